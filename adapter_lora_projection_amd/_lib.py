@@ -88,6 +88,18 @@ SIGNATURES = {
     "lora_qkv_workspace_size": (_sz, [_i32, _i64, _i64, _i64, _i64, _i32]),
     "lora_embedding_a": (_i32, [_i32, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _i64, _i64, _i64,
                                 _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "lora_linear_w4_prepared_size": (_sz, [_i32, _i64, _i64, _i32, _i32]),
+    "lora_linear_w4_prepare": (_i32, [_i32, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                                      _sz, _vp]),
+    "lora_linear_w4": (_i32, [_i32, _i64, _i64, _i64, _i32, _i32, _vp, _i64, _vp, _vp, _i64, _vp]),
+    "lora_rope_append": (_i32, [_i32, _i64, _i32, _i32, _i32, _i32, _i32, _i64, _i32, _i64, _vp,
+                                _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp,
+                                ctypes.c_float, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _vp]),
+    "lora_prefix_attention": (_i32, [_i32, _i64, _i32, _i32, _i32, _i32, _i64, _i32, _vp, _i64, _vp,
+                                     _vp, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _i64,
+                                     _vp, ctypes.c_float, _vp, _i64, _vp, _vp, _sz, _vp]),
+    "lora_prefix_attention_workspace_size": (_sz, [_i32, _i64, _i32, _i32, _i32, _i32, _i32, _i64,
+                                                   _i64]),
 }
 
 
@@ -358,3 +370,50 @@ def lora_check_metadata(T, G, L, R, S, N, seg_indptr, weight_indices, permutatio
 
 def lora_check_metadata_workspace_size(T) -> int:
     return int(lib().lora_check_metadata_workspace_size(T))
+
+
+def lora_linear_w4_prepared_size(dtype, K, N, group, zero_points) -> int:
+    return int(lib().lora_linear_w4_prepared_size(dtype, K, N, group, zero_points))
+
+
+def lora_linear_w4_prepare(dtype, K, N, group, codes, ldc, scales, lds, zero_points, ldz, prepared,
+                           prepared_bytes, stream) -> None:
+    st = lib().lora_linear_w4_prepare(dtype, K, N, group, _p(codes), ldc, _p(scales), lds,
+                                      _p(zero_points), ldz, _p(prepared), prepared_bytes, stream)
+    _check("lora_linear_w4_prepare", st)
+
+
+def lora_linear_w4(dtype, M, K, N, group, zero_points, x, ldx, prepared, y, ldy, stream) -> None:
+    st = lib().lora_linear_w4(dtype, M, K, N, group, zero_points, _p(x), ldx, _p(prepared), _p(y),
+                              ldy, stream)
+    _check("lora_linear_w4", st)
+
+
+def lora_rope_append(dtype, T, Hq, Hkv, D, rot, interleaved, num_pages, page_size, table_rows, q,
+                     ldq, k, ldk, v, ldv, table, positions, slots, q_norm, k_norm, eps, q_out, ldqo,
+                     k_cache, v_cache, page_stride, token_stride, head_stride, stream) -> None:
+    st = lib().lora_rope_append(dtype, T, Hq, Hkv, D, rot, interleaved, num_pages, page_size,
+                                table_rows, _p(q), ldq, _p(k), ldk, _p(v), ldv, _p(table),
+                                _p(positions), _p(slots), _p(q_norm), _p(k_norm), eps, _p(q_out),
+                                ldqo, _p(k_cache), _p(v_cache), page_stride, token_stride,
+                                head_stride, stream)
+    _check("lora_rope_append", st)
+
+
+def lora_prefix_attention(dtype, T, G, Hq, Hkv, D, num_pages, page_size, q, ldq, k_cache, v_cache,
+                          page_stride, token_stride, head_stride, seg_indptr, permutation,
+                          prefix_pages, prefix_width, prefix_lens, own_pages, own_width, own_lens,
+                          scale, out, ldo, lse, workspace, workspace_bytes, stream) -> None:
+    st = lib().lora_prefix_attention(dtype, T, G, Hq, Hkv, D, num_pages, page_size, _p(q), ldq,
+                                     _p(k_cache), _p(v_cache), page_stride, token_stride,
+                                     head_stride, _p(seg_indptr), _p(permutation),
+                                     _p(prefix_pages), prefix_width, _p(prefix_lens),
+                                     _p(own_pages), own_width, _p(own_lens), scale, _p(out), ldo,
+                                     _p(lse), _p(workspace), workspace_bytes, stream)
+    _check("lora_prefix_attention", st)
+
+
+def lora_prefix_attention_workspace_size(dtype, T, G, Hq, Hkv, D, page_size, prefix_width,
+                                         own_width) -> int:
+    return int(lib().lora_prefix_attention_workspace_size(dtype, T, G, Hq, Hkv, D, page_size,
+                                                          prefix_width, own_width))

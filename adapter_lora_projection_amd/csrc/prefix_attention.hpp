@@ -1,0 +1,43 @@
+// Internal launch interface of the shared-prefix attention kernels (not part of the public C ABI).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace lmx {
+
+struct PrefixAttnArgs {
+  const void* q;        // [T][ldq], head h of token t at t * ldq + h * D
+  const void* k_cache;  // element (page, place, head, d) at page * page_stride + place *
+  const void* v_cache;  //   token_stride + head * head_stride + d, the same for both
+  const int* seg_indptr;
+  const int* permutation;   // null: identity
+  const int* prefix_pages;  // [G][prefix_width]
+  const int* prefix_lens;   // [G] (null: no prefixes)
+  const int* own_pages;     // [T][own_width]
+  const int* own_lens;      // [T] (null: no keys of their own)
+  void* out;                // [T][ldo]
+  float* lse;               // [T][Hq] or null
+  float* part_o;            // [slots][T * Hq][D]: unnormalised outputs of each key range
+  float2* part_ml;          // [slots][T * Hq]: running maximum (base 2) and sum of each
+  int64_t ldq, ldo, page_stride, token_stride, head_stride;
+  int T, G, Hq, Hkv, grp, D, page_size, num_pages, prefix_width, own_width;
+  int prefix_tiles, prefix_splits;  // row-tile bound and key ranges of the prefix part
+  int own_tiles, own_splits;        // row tiles per token and key ranges of the own part
+  float scale_log2;                 // scale * log2(e)
+};
+
+// Launch plan from host-known sizes only (lengths live on the device; the page lists' widths bound
+// them).
+struct PrefixAttnPlan {
+  int dp;  // head size rounded up to 64, 128 or 256
+  int prefix_tiles, prefix_splits, own_tiles, own_splits;
+  size_t part_ml, total;  // workspace: byte offset of part_ml, total bytes
+};
+PrefixAttnPlan prefix_attention_plan(int64_t T, int G, int Hq, int Hkv, int D, int page_size,
+                                     int64_t prefix_width, int64_t own_width);
+
+hipError_t launch_prefix_attention(int dtype, const PrefixAttnPlan& plan, const PrefixAttnArgs& a,
+                                   hipStream_t st);
+
+}  // namespace lmx

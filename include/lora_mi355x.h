@@ -17,6 +17,9 @@
  *     and query/key/value of one x) of the same fast path (pull request 9754).
  *   - lora_embedding_a: the embedding LoRA-A product of the same LoRA op family (pull request
  *     550), sized without a longest-segment bound.
+ *   - lora_linear_w4, lora_rope_append, lora_prefix_attention: the rest of a decode step's attention
+ *     layer around the projections: the 4-bit base product that the adapters update, the rotation
+ *     and cache append after it, and the attention over a prefix shared by an adapter's tokens.
  *   - lora_schedule_tiles: export of the device segment schedule (the on-device segment scheduler
  *     named in the Summary of pull request 550) for checking.
  *   - lora_check_metadata: the value checks that pull request 550 (Behaviour changes) moves out of
@@ -557,6 +560,144 @@ lora_status lora_embedding_a(lora_dtype dtype, int64_t T, int64_t V, int32_t R, 
                              const int32_t* seg_indptr, const int32_t* weight_indices,
                              const int32_t* permutation, const int32_t* lora_ranks, void* h,
                              int64_t ldh, void* stream);
+
+/*
+ * lora_linear_w4 -- projection with 4-bit weights and group scales, for few rows of x: the base
+ * product y = x W^T of a quantised layer, which lora_shrink_expand then updates in place.
+ *
+ *   y[m][n] = round( sum_{k<K} x[m][k] W[n][k] ),
+ *   W[n][k] = scales[n][k / group] * (c[n][k] - z[n][k / group]),
+ * c and z in 0..15 (z = 8 without zero points), with fp32 accumulation and one rounding to `dtype`.
+ * Few rows is where it is fast (the time is that of reading the weight up to about 16 rows); any M
+ * is right. x has to be finite: an infinity gives NaN in its row.
+ *
+ * lora_linear_w4_prepare writes the weight in the layout the product reads, once per layer:
+ *   dtype          LORA_BF16 or LORA_F16: the type of x, y and scales.
+ *   K, N, group    input and output features, codes per scale: 32, 64 or 128; K % group == 0.
+ *   codes          device [N][ldc] bytes, ldc >= K / 2: byte k / 2 of row n holds the code of an even k
+ *                  in its low half and that of k + 1 in its high half.
+ *   scales         device [N][lds], lds >= K / group.
+ *   zero_points    device [N][ldz] bytes (the low 4 bits count), ldz >= K / group; NULL: 8 everywhere.
+ *   prepared       device, >= lora_linear_w4_prepared_size(...) bytes, 16-byte aligned; the inputs are
+ *                  not needed afterwards.
+ * lora_linear_w4 takes the same dtype, K, N, group and presence of zero points, and
+ *   x [M][ldx >= K], 16-byte aligned rows; y [M][ldy >= N], any alignment (not accumulated into; must
+ *   not overlap x). No workspace, one launch.
+ * Errors: LORA_EUNSUPPORTED (dtype, group, K or N above 2^24, M above 2^20, unaligned x or
+ * prepared), LORA_EINVAL (sizes, K % group, pitches, null pointers), LORA_EWORKSPACE (prepared too
+ * small), LORA_EHIP. lora_linear_w4_prepared_size returns 0 for sizes that are refused.
+ */
+lora_status lora_linear_w4_prepare(lora_dtype dtype, int64_t K, int64_t N, int32_t group,
+                                   const uint8_t* codes, int64_t ldc, const void* scales,
+                                   int64_t lds, const uint8_t* zero_points, int64_t ldz,
+                                   void* prepared, size_t prepared_bytes, void* stream);
+
+size_t lora_linear_w4_prepared_size(lora_dtype dtype, int64_t K, int64_t N, int32_t group,
+                                    int32_t zero_points);
+
+lora_status lora_linear_w4(lora_dtype dtype, int64_t M, int64_t K, int64_t N, int32_t group,
+                           int32_t zero_points, const void* x, int64_t ldx, const void* prepared,
+                           void* y, int64_t ldy, void* stream);
+
+/*
+ * lora_rope_append -- what follows a q/k/v projection: the rotation of queries and keys (with an
+ * optional norm of each head before it), and the append of keys and values to a paged cache.
+ *
+ * For token t and every head h of q and of k, D elements each:
+ *     u = x * w / sqrt(mean(x^2) + eps)   (w = q_norm or k_norm; u = x where it is NULL)
+ *     (u_a, u_b) <- (u_a c_p - u_b s_p, u_b c_p + u_a s_p),  p < rot / 2,
+ * (a, b) = (p, p + rot / 2), or (2p, 2p + 1) when interleaved; elements from rot on pass. All in
+ * fp32, rounded once to `dtype`. q goes to q_out, k to the cache place of slots[t], and v is copied
+ * there bit for bit.
+ *
+ *   dtype          LORA_F32, LORA_BF16 or LORA_F16: q, k, v, norms, q_out and caches.
+ *   T, Hq, Hkv, D  tokens, query heads (0: no queries), key/value heads, head size (1 .. 1024).
+ *   rot            rotated elements of a head, even, 2 <= rot <= D.
+ *   q, k, v        device [T][ldq >= Hq*D], [T][ldk >= Hkv*D], [T][ldv >= Hkv*D] (column views of one
+ *                  fused projection, for instance).
+ *   table          device float [table_rows][rot]: row p holds rot / 2 cosines, then rot / 2 sines.
+ *   positions      device int32 [T]: table row of each token. A token whose position is outside
+ *                  [0, table_rows) is left out entirely (q_out row and cache stay as they were).
+ *   slots          device int64 [T]: place page * page_size + offset in the cache; a slot outside
+ *                  [0, num_pages * page_size), such as -1 of a padding row, appends nothing. Of
+ *                  tokens that share a slot, any may win, element by element.
+ *   q_norm, k_norm device [D] or NULL; eps >= 0.
+ *   q_out          device [T][ldqo >= Hq*D]; may be q itself (same pitch), else must not overlap q.
+ *   k_cache,       device; element (page, place, head, d) at page * page_stride + place *
+ *   v_cache        token_stride + head * head_stride + d of either (element strides >= 0, no two
+ *                  places overlapping), so that both [page][place][head][d] and
+ *                  [page][head][place][d] storage fit.
+ * Any alignment; rows, weights and cache rows that are all 16-byte aligned, with D % 8 == 0 and
+ * rot % 16 == 0, take the vector form. One launch, no workspace.
+ * Errors: LORA_EUNSUPPORTED (dtype, D > 1024, T * (Hq + 2 Hkv) > 2^30), LORA_EINVAL (sizes, strides,
+ * eps, null pointers), LORA_EHIP.
+ */
+lora_status lora_rope_append(lora_dtype dtype, int64_t T, int32_t Hq, int32_t Hkv, int32_t D,
+                             int32_t rot, int32_t interleaved, int64_t num_pages,
+                             int32_t page_size, int64_t table_rows, const void* q, int64_t ldq,
+                             const void* k, int64_t ldk, const void* v, int64_t ldv,
+                             const float* table, const int32_t* positions, const int64_t* slots,
+                             const void* q_norm, const void* k_norm, float eps, void* q_out,
+                             int64_t ldqo, void* k_cache, void* v_cache, int64_t page_stride,
+                             int64_t token_stride, int64_t head_stride, void* stream);
+
+/*
+ * lora_prefix_attention -- attention of one query token per row over a paged cache, where the tokens
+ * of a segment share a prefix (a system prompt, say). Keys and values of a prompt depend on the
+ * adapter, so the segments of the multi-adapter calls are what can share them; their metadata is
+ * used as it is. The shared keys are read once for the segment's rows, not once per token.
+ *
+ * For segment g and sorted position i in it, t = permutation[i], the keys are places 0 ..
+ * prefix_lens[g] - 1 of the page list prefix_pages[g], then places 0 .. own_lens[t] - 1 of
+ * own_pages[t]. For query head h (key head h / (Hq / Hkv)):
+ *     s_j = scale * (q[t][h] . k_j),   m = max_j s_j,   lse[t][h] = m + log(sum_j exp(s_j - m)),
+ *     out[t][h] = round( sum_j exp(s_j - m) v_j / sum_j exp(s_j - m) ).
+ * A row without a key gets zeros and lse = -inf. Scores, maxima, sums and partial outputs are fp32;
+ * the weights exp(s_j - m) are rounded to `dtype` for the product with v_j, in the sum as well.
+ * Several tokens of one sequence (a chunk of a prompt, tokens to verify) are rows that repeat the
+ * page list with own_lens rising by one.
+ *
+ *   dtype          LORA_BF16 or LORA_F16.
+ *   T, G           query tokens, segments.
+ *   Hq, Hkv, D     query heads, key/value heads (Hq % Hkv == 0), head size: D % 8 == 0, D <= 256.
+ *   num_pages,     pages of the caches and places per page (any size).
+ *   page_size
+ *   q              device [T][ldq >= Hq*D], 16-byte aligned rows, token order.
+ *   k_cache,       device, strides as for lora_rope_append, rows of D 16-byte aligned. Places that
+ *   v_cache        no list names within its length are never used in the result, whatever they hold.
+ *   seg_indptr,    as for lora_shrink; rows of out (and lse) that no segment covers are not written.
+ *   permutation
+ *   prefix_pages   device int32 [G][prefix_width]; prefix_lens device int32 [G]. Both NULL with
+ *                  prefix_width 0: no shared prefixes.
+ *   own_pages      device int32 [T][own_width], own_lens device int32 [T], token order. Both NULL with
+ *                  own_width 0.
+ *                  Lengths are clamped to [0, width * page_size]. The places of a page id outside
+ *                  [0, num_pages) are masked; entries beyond a list's length are not read.
+ *   out            device [T][ldo >= Hq*D], any alignment.
+ *   lse            device float [T][Hq] (natural logarithm) or NULL.
+ *   workspace      device scratch of lora_prefix_attention_workspace_size(...) bytes (partial outputs
+ *                  of the key ranges), 16-byte aligned; not read before written. Calls that overlap in
+ *                  time must not share it.
+ * The number of key ranges follows from the widths, so pass lists no wider than the longest length
+ * needs. Results do not depend on timing.
+ * Errors: LORA_EUNSUPPORTED (dtype, D, unaligned q or cache, width * page_size > 2^30,
+ * T * Hq > 2^26), LORA_EINVAL (sizes, strides, a scale that is not finite, null pointers),
+ * LORA_EWORKSPACE, LORA_EHIP.
+ */
+lora_status lora_prefix_attention(lora_dtype dtype, int64_t T, int32_t G, int32_t Hq, int32_t Hkv,
+                                  int32_t D, int64_t num_pages, int32_t page_size, const void* q,
+                                  int64_t ldq, const void* k_cache, const void* v_cache,
+                                  int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                                  const int32_t* seg_indptr, const int32_t* permutation,
+                                  const int32_t* prefix_pages, int64_t prefix_width,
+                                  const int32_t* prefix_lens, const int32_t* own_pages,
+                                  int64_t own_width, const int32_t* own_lens, float scale,
+                                  void* out, int64_t ldo, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+size_t lora_prefix_attention_workspace_size(lora_dtype dtype, int64_t T, int32_t G, int32_t Hq,
+                                            int32_t Hkv, int32_t D, int32_t page_size,
+                                            int64_t prefix_width, int64_t own_width);
 
 /*
  * lora_check_metadata -- the value checks of the LoRA metadata that "Decode LoRA kernels are

@@ -27,10 +27,12 @@ from .mlp import silu, lora_mlp, lora_mlp_rows, sigmoid, silu_grad, lora_mlp_sav
     lora_mlp_grads
 from .linear import lora_linear, lora_qkv, lora_linear_rows, lora_linear_backward, lora_qkv_backward
 from .embedding import embedding_lora_a
+from .decode import linear_w4, prefix_attention, rope_append, rope_head, w4_weight
 
 __all__ = [
     "rho", "DTYPE_FORMATS", "shrink", "expand", "tile_list", "slice_blocks",
     "validate_metadata", "silu", "lora_mlp", "lora_mlp_rows", "sigmoid", "silu_grad",
     "lora_mlp_saved", "lora_mlp_backward", "lora_mlp_grads", "lora_linear", "lora_qkv",
     "lora_linear_rows", "lora_linear_backward", "lora_qkv_backward", "embedding_lora_a",
+    "w4_weight", "linear_w4", "rope_head", "rope_append", "prefix_attention",
 ]
