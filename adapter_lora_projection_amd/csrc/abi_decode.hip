@@ -3,6 +3,7 @@
 // host before anything is enqueued; nothing reads device memory.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -208,7 +209,11 @@ lora_status lora_prefix_attention(lora_dtype dtype, int64_t T, int32_t G, int32_
   a.prefix_width = int(prefix_width); a.own_width = int(own_width);
   a.prefix_tiles = p.prefix_tiles; a.prefix_splits = p.prefix_splits;
   a.own_tiles = p.own_tiles; a.own_splits = p.own_splits;
-  a.scale_log2 = float(double(scale) * 1.4426950408889634);
+  a.shared = p.shared; a.prefix_unit = p.prefix_unit; a.own_unit = p.own_unit;
+  // the kernels multiply masked scores (-inf) by it: above 0, with the sign in the queries (a scale of
+  // 0 gives equal weights, and so does 2^-100)
+  a.negate = scale < 0.f;
+  a.scale_log2 = std::max(std::fabs(scale) * 1.44269504f, 0x1p-100f);
   return hip_status(lmx::launch_prefix_attention(dtype, p, a, reinterpret_cast<hipStream_t>(stream)));
 }
 

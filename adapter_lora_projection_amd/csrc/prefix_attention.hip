@@ -4,24 +4,33 @@
 // For sorted position i (token t = perm[i], segment g) and query head h, over the keys j of the
 // segment's prefix followed by the token's own:
 //     s_j = scale q_t,h . k_j,   o = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),   m = max_j s_j.
-// Every (row tile, key head, key range) is one workgroup; its waves take 32-key blocks of the range
-// in turn, each with its own running maximum and sum (fp32, base 2), and are joined in LDS at the
-// end. The ranges of a row are joined by a second kernel with the same rule. A prefix tile holds 16
-// query rows (token, head of the group) of one segment, so the prefix is read once per 16 rows;
-// an own tile holds the query heads of one token.
+// Every (row tile, key head, key range) is one workgroup; the ranges of a row are joined by a second
+// kernel. Statistics and outputs are fp32, scores in base 2. Two kinds of tiles run in one launch:
 //
-// Matrix steps (v_mfma_f32_16x16x32): scores transposed, S^T = K Q^T (K rows as the A operand, the
-// queries as columns), so that a lane holds 4 + 4 scores of ONE query and the softmax needs two
-// cross-lane steps per block; O^T = V^T P^T takes those 8 probabilities as its B operand as they
-// lie (keys 4g + i and 16 + 4g + i of lane group g; the contraction order is free as long as V uses
-// the same), and V^T is read from the row-major block by the transposing LDS read.
+//   shared (tile_body)  128 query rows (token, head of the group) of one segment against a range of
+//     its prefix, when segments have more than 32 rows on average: 4 waves of 32 rows walk the same
+//     64-key blocks (32 for D > 128), staged once in LDS. The arithmetic of the prefix is bound by
+//     the matrix and exponential pipes and by LDS reads (64 rows x 128 keys of a block cost as many
+//     LDS cycles as matrix cycles).
+//   rows (rows_body)    at most 16 rows: the heads of one token against its own keys, or the rows of a
+//     short prefix tile. Bound by the bytes of the keys: each wave takes 16-key blocks of the range
+//     in turn, with its own statistics, and the waves are joined in LDS at the end.
+//
+// Prefix workgroups come first, about one per compute unit, and leave half of each unit's LDS to
+// the memory-bound ones that follow, which then run beside them.
+//
+// Matrix steps: scores transposed, S^T = K Q^T (K rows as the A operand, the queries as columns),
+// so that a lane holds scores of ONE query and the softmax needs one or two cross-lane steps per
+// block; O^T = V^T P^T takes those probabilities as its B operand as they lie (the contraction
+// order over the keys is free as long as V uses the same), and V^T is read from the row-major block
+// by the transposing LDS read.
 // P is rounded to the storage type for the second product, and the sum of a row adds the rounded
-// values, so the weights applied are normalised exactly; scores, maxima, sums and outputs are fp32.
+// values, so the weights applied are normalised exactly.
 //
 // Keys and values go straight from the cache to LDS (16 bytes a lane); the addresses come from a
-// per-wave table of 256 key offsets in LDS, so that no page-list load sits in the way of the
-// loads in flight. The 16-byte chunks of a key row are XOR-swizzled by the row (by the choice of
-// the global chunk each lane fetches) so that 16 rows at one chunk spread over the banks.
+// table of key offsets in LDS, so that no page-list load sits in the way of the loads in flight. The
+// 16-byte chunks of a key row are XOR-swizzled by the row (by the choice of the global chunk each
+// lane fetches) so that rows at one chunk spread over the banks.
 // A key whose page id lies outside the cache, or beyond its list's length, is masked: its offset is
 // -1, its row is filled from a zero vector and its score is -inf.
 #include <algorithm>
@@ -37,8 +46,9 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 __device__ const uint4 kZeroChunk = {0u, 0u, 0u, 0u};
 
-constexpr int kBlk = 32;       // keys per block
-constexpr int kTabBlocks = 8;  // blocks covered by one fill of the offset table
+// The base of the exponentials follows the running maximum only when it lags by more than 2^4: weights
+// up to 16 cost nothing in a floating type, and the outputs are rescaled a few times per range.
+constexpr float kLag = 4.f;
 
 constexpr float kNegInf = -__builtin_huge_valf();
 
@@ -56,6 +66,63 @@ __device__ __forceinline__ uint4 lds_read16(uint32_t addr) {
   return make_uint4(v.x, v.y, v.z, v.w);
 }
 
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+template <int DT>
+__device__ __forceinline__ f32x16_t mma32(uint4 a, uint4 b, f32x16_t acc) {
+  if constexpr (DT == DT_BF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                   __builtin_bit_cast(bf16x8_t, b), acc, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a),
+                                                  __builtin_bit_cast(f16x8_t, b), acc, 0, 0, 0);
+}
+
+// Two fp32 values rounded to nearest even to the storage type, one instruction.
+template <int DT>
+__device__ __forceinline__ uint32_t cvt2(float a, float b) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  const f2 v = {a, b};
+  if constexpr (DT == DT_BF16) {
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, b2));
+  } else {
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, h2));
+  }
+}
+
+// acc + lo + hi of a packed pair, in fp32.
+template <int DT>
+__device__ __forceinline__ float add2(uint32_t p, float acc) {
+  if constexpr (DT == DT_BF16) {
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, p), __builtin_bit_cast(b2, 0x3f803f80u), acc, false);
+  } else {
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(h2, p), __builtin_bit_cast(h2, 0x3c003c00u), acc, false);
+  }
+}
+
+// Eight query elements, negated for a negative scale (the kernels use its magnitude).
+__device__ __forceinline__ uint4 signed_chunk(uint4 v, int negate) {
+  const uint32_t f = negate ? 0x80008000u : 0u;
+  return make_uint4(v.x ^ f, v.y ^ f, v.z ^ f, v.w ^ f);
+}
+
+// Maximum over the two lanes l and l ^ 32.
+__device__ __forceinline__ float max_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float add_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+constexpr int kTileRows = 128;  // query rows of a shared tile: 32 per wave
+constexpr int kRows = 16;       // of the others
+
 // What one workgroup computes: rows of one segment or token, one key head, one key range.
 struct Work {
   const int* pages;  // page list of the keys
@@ -64,7 +131,7 @@ struct Work {
   int row0, nrows;   // flattened rows (sorted position * grp + head of the group) of the tile
   int slot;          // partial slot
   int kvh;
-  bool live;
+  bool live, shared;
 };
 
 __device__ __forceinline__ int clamp_len(int len, int width, int page) {
@@ -80,6 +147,13 @@ __device__ __forceinline__ void key_range(int len, int n, int s, int unit, int* 
   *k1 = int(min(lo + per, int64_t(len)));
 }
 
+// Number of key ranges that hold keys (the first ones).
+__device__ __forceinline__ int ranges_used(int len, int n, int unit) {
+  if (n == 0 || len == 0) return 0;
+  const int per = ((len + n - 1) / n + unit - 1) / unit * unit;
+  return (len + per - 1) / per;
+}
+
 __device__ __forceinline__ int seg_lo(const PrefixAttnArgs& a, int g) {
   return min(max(a.seg_indptr[g], 0), a.T);
 }
@@ -87,10 +161,10 @@ __device__ __forceinline__ int seg_lo(const PrefixAttnArgs& a, int g) {
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // Decodes blockIdx into a Work. Prefix workgroups come first (they are the longest).
-template <int ROWS, int UNIT>
 __device__ __forceinline__ Work find_work(const PrefixAttnArgs& a, int b) {
   Work w{};
   const int np = a.prefix_tiles * a.prefix_splits * a.Hkv;
+  const int ROWS = a.shared ? kTileRows : kRows;
   if (b < np) {
     w.kvh = b % a.Hkv;
     const int rest = b / a.Hkv;
@@ -123,8 +197,9 @@ __device__ __forceinline__ Work find_work(const PrefixAttnArgs& a, int b) {
         w.nrows = min(ROWS, n_s * a.grp - r0);
         w.pages = a.prefix_pages + int64_t(gs) * a.prefix_width;
         w.len = clamp_len(a.prefix_lens[gs], a.prefix_width, a.page_size);
-        key_range(w.len, a.prefix_splits, w.slot, UNIT, &w.k0, &w.k1);
+        key_range(w.len, a.prefix_splits, w.slot, a.prefix_unit, &w.k0, &w.k1);
         w.live = w.k1 > w.k0;
+        w.shared = a.shared != 0;
         return w;
       }
       tile -= uniform(__shfl(incl, 63, 64));
@@ -142,50 +217,119 @@ __device__ __forceinline__ Work find_work(const PrefixAttnArgs& a, int b) {
   const int tok = a.permutation != nullptr ? a.permutation[i] : i;
   if (tok < 0 || tok >= a.T) return w;
   w.slot = a.prefix_splits + split;
-  w.row0 = i * a.grp + tile * ROWS;
-  w.nrows = min(ROWS, a.grp - tile * ROWS);
+  w.row0 = i * a.grp + tile * kRows;
+  w.nrows = min(kRows, a.grp - tile * kRows);
   w.pages = a.own_pages + int64_t(tok) * a.own_width;
   w.len = clamp_len(a.own_lens[tok], a.own_width, a.page_size);
-  key_range(w.len, a.own_splits, split, UNIT, &w.k0, &w.k1);
+  key_range(w.len, a.own_splits, split, a.own_unit, &w.k0, &w.k1);
   w.live = w.k1 > w.k0;
   return w;
 }
 
 template <int DT>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  return uint32_t(Traits<DT>::from_f32(a)) | (uint32_t(Traits<DT>::from_f32(b)) << 16);
+__device__ __forceinline__ f32x4_t mma16(uint2 a, uint2 b, f32x4_t acc) {
+  if constexpr (DT == DT_BF16) {
+    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4_t, a),
+                                                     __builtin_bit_cast(s16x4_t, b), acc, 0, 0, 0);
+  } else {
+    typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
+    return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(f16x4_t, a),
+                                                 __builtin_bit_cast(f16x4_t, b), acc, 0, 0, 0);
+  }
 }
 
-// LDS of one wave: two buffers of a K and a V block, the key offset table and the block masks.
+// Maximum over the lanes l ^ 16 k.
+__device__ __forceinline__ float max_groups(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return max_halves(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ __forceinline__ float add_groups(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return add_halves(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
+
+constexpr int kWaves = 4;
+constexpr int kTabKeys = 256;  // keys covered by one fill of a wave's offset table
+
+// Row tile of at most 16 query rows, its keys split over the waves in 16-key blocks. LDS of one wave:
+// a ring of K and V blocks, the offsets of its next 256 keys and their validity.
 template <int DP>
-struct WaveLds {
-  uint16_t kv[2][2][kBlk * DP];
-  int64_t off[kTabBlocks * kBlk];
-  uint32_t mask[kTabBlocks];
+struct RowsWave {
+  static constexpr int kBufs = DP > 64 ? 2 : 4;
+  uint16_t kv[kBufs][2][16 * DP];
+  int64_t off[kTabKeys];
+  uint64_t mask[kTabKeys / 64];
+};
+template <int DP>
+struct RowsLds {
+  RowsWave<DP> wave[kWaves];
+  float2 ml[kWaves][16];
 };
 
-template <int DP>
-constexpr int attn_waves() { return DP > 128 ? 2 : 4; }
-
 template <int DT, int DP>
-__global__ __launch_bounds__(64 * attn_waves<DP>()) void prefix_attn_kernel(PrefixAttnArgs a) {
-  constexpr int NW = attn_waves<DP>();
+__device__ __forceinline__ void rows_body(const PrefixAttnArgs& a, const Work& w, RowsLds<DP>& S) {
+  constexpr int NB = RowsWave<DP>::kBufs;
   constexpr int CPR = DP / 8;         // 16-byte chunks per key row
   constexpr int RPI = 64 / CPR;       // key rows one DMA instruction covers
-  constexpr int NI = kBlk / RPI;      // DMA instructions per block and operand
+  constexpr int NI = 16 / RPI;        // DMA instructions per block and operand
   constexpr int KS = DP / 32;         // reduction steps of the scores
   constexpr int DTILES = DP / 16;     // 16-row tiles of O^T
-  __shared__ __align__(16) WaveLds<DP> s_wave[NW];
-  __shared__ float2 s_ml[NW][16];
-
-  const Work w = find_work<16, kBlk * NW>(a, int(blockIdx.x));
-  if (!w.live) return;
+  constexpr int TB = kTabKeys / 16;
 
   const int lane = int(threadIdx.x) & 63, wave = wave_id();
   const int col = lane & 15, grp = lane >> 4;
-  WaveLds<DP>& L = s_wave[wave];
+  RowsWave<DP>& L = S.wave[wave];
   const uint16_t* kc = static_cast<const uint16_t*>(a.k_cache);
   const uint16_t* vc = static_cast<const uint16_t*>(a.v_cache);
+
+  const int nblk = (w.k1 - w.k0 + 15) / 16;
+  const int mine = (nblk - wave + kWaves - 1) / kWaves;  // blocks wave, wave + 4, ...
+
+  // offsets and validity of this wave's blocks first .. first + TB - 1
+  auto fill_table = [&](int first) {
+#pragma unroll
+    for (int e = 0; e < kTabKeys / 64; ++e) {
+      const int idx = e * 64 + lane;
+      const int key = w.k0 + ((first + (idx >> 4)) * kWaves + wave) * 16 + (idx & 15);
+      int64_t off = -1;
+      if (key < w.k1) {
+        const int pg = key / a.page_size, place = key - pg * a.page_size;
+        const int id = w.pages[pg];
+        if (id >= 0 && id < a.num_pages)
+          off = int64_t(id) * a.page_stride + int64_t(place) * a.token_stride +
+                int64_t(w.kvh) * a.head_stride;
+      }
+      L.off[idx] = off;
+      const unsigned long long bits = __ballot(off >= 0);
+      if (lane == 0) L.mask[e] = bits;
+    }
+    // the reads below are other lanes' writes (LDS operations of one wave complete in order)
+    __builtin_amdgcn_wave_barrier();
+    asm volatile("" ::: "memory");
+  };
+  auto issue = [&](int j) {
+    const int tb = j % TB, buf = j % NB;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = i * RPI + lane / CPR;
+      const int64_t off = L.off[tb * 16 + r];
+      const int cs = lane % CPR;
+      const int ck = cs ^ (r & (CPR - 1)), cv = cs ^ (((r & 7) << 1) & (CPR - 1));
+      const bool ok = off >= 0;
+      const void* kp = ok && ck * 8 < a.D ? static_cast<const void*>(kc + off + ck * 8) : &kZeroChunk;
+      const void* vp = ok && cv * 8 < a.D ? static_cast<const void*>(vc + off + cv * 8) : &kZeroChunk;
+      dma16(kp, __builtin_amdgcn_readfirstlane(lds_addr(&L.kv[buf][0][i * 512])));
+      dma16(vp, __builtin_amdgcn_readfirstlane(lds_addr(&L.kv[buf][1][i * 512])));
+    }
+  };
+  // A block whose issue crosses into the next table fill finds the table free: the masks of earlier
+  // blocks are read when they are issued.
+  uint32_t masks[NB];
+  auto start = [&](int j, uint32_t& mask) {
+    if (j % TB == 0) fill_table(j);
+    mask = uint32_t(uniform(int(uint32_t(L.mask[(j % TB) / 4] >> (16 * (j & 3)))))) & 0xffffu;
+    issue(j);
+  };
 
   // the query column of this lane
   const bool row_ok = col < w.nrows;
@@ -201,176 +345,316 @@ __global__ __launch_bounds__(64 * attn_waves<DP>()) void prefix_attn_kernel(Pref
     for (int s = 0; s < KS; ++s) {
       const int d = s * 32 + grp * 8;
       qf[s] = make_uint4(0u, 0u, 0u, 0u);
-      if (tok_ok && d < a.D) qf[s] = gload16(qp + d);
+      if (tok_ok && d < a.D) qf[s] = signed_chunk(gload16(qp + d), a.negate);
     }
   }
-
   f32x4_t o[DTILES];
 #pragma unroll
   for (int t = 0; t < DTILES; ++t) o[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   float m = kNegInf, l = 0.f;
 
-  const int nblk = (w.k1 - w.k0 + kBlk - 1) / kBlk;
-  const int mine = (nblk - wave + NW - 1) / NW;  // blocks wave, wave + NW, ...
-
-  // offsets and masks of this wave's blocks first .. first + kTabBlocks - 1
-  auto fill_table = [&](int first) {
-#pragma unroll
-    for (int e = 0; e < kTabBlocks * kBlk / 64; ++e) {
-      const int idx = e * 64 + lane;
-      const int key = w.k0 + ((first + (idx >> 5)) * NW + wave) * kBlk + (idx & 31);
-      int64_t off = -1;
-      if (key < w.k1) {
-        const int pg = key / a.page_size, place = key - pg * a.page_size;
-        const int id = w.pages[pg];
-        if (id >= 0 && id < a.num_pages)
-          off = int64_t(id) * a.page_stride + int64_t(place) * a.token_stride +
-                int64_t(w.kvh) * a.head_stride;
-      }
-      L.off[idx] = off;
-      const unsigned long long bits = __ballot(off >= 0);
-      if (lane == 0) {
-        L.mask[2 * e] = uint32_t(bits);
-        L.mask[2 * e + 1] = uint32_t(bits >> 32);
-      }
-    }
-    // the reads below are other lanes' writes (LDS operations of one wave complete in order)
-    __builtin_amdgcn_wave_barrier();
-    asm volatile("" ::: "memory");
-  };
-  // issues the loads of table block `tb` into buffer `buf`
-  auto issue = [&](int tb, int buf) {
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int r = i * RPI + lane / CPR;
-      const int64_t off = L.off[tb * kBlk + r];
-      const int cs = lane % CPR;
-      const int ck = cs ^ (r & (CPR - 1)), cv = cs ^ ((r & 7) << 1 & (CPR - 1));
-      const bool ok = off >= 0;
-      const void* kp = ok && ck * 8 < a.D ? static_cast<const void*>(kc + off + ck * 8) : &kZeroChunk;
-      const void* vp = ok && cv * 8 < a.D ? static_cast<const void*>(vc + off + cv * 8) : &kZeroChunk;
-      dma16(kp, __builtin_amdgcn_readfirstlane(lds_addr(&L.kv[buf][0][i * 512])));
-      dma16(vp, __builtin_amdgcn_readfirstlane(lds_addr(&L.kv[buf][1][i * 512])));
-    }
-  };
-
-  if (mine > 0) {
-    fill_table(0);
-    issue(0, 0);
-  }
-  for (int j = 0; j < mine; ++j) {
-    const int buf = j & 1;
-    const uint32_t mask = __builtin_amdgcn_readfirstlane(L.mask[j % kTabBlocks]);
-    if (j + 1 < mine) {
-      if ((j + 1) % kTabBlocks == 0) fill_table(j + 1);
-      issue((j + 1) % kTabBlocks, buf ^ 1);
-      vm_wait<2 * NI>();
-    } else {
-      vm_wait<0>();
-    }
-    asm volatile("" ::: "memory");
+  auto compute = [&](int buf, uint32_t mask) {
     const uint32_t kb = lds_addr(&L.kv[buf][0][0]), vb = lds_addr(&L.kv[buf][1][0]);
-    // scores of 2 x 16 keys
-    f32x4_t sc[2];
+    f32x4_t sc = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      sc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      const int r = t * 16 + col;
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const int c = (s * 4 + grp) ^ (r & (CPR - 1));
-        sc[t] = mma_step<DT>(lds_read16(kb + uint32_t(r * DP * 2 + c * 16)), qf[s], sc[t]);
-      }
+    for (int s = 0; s < KS; ++s) {
+      const int c = (s * 4 + grp) ^ (col & (CPR - 1));
+      sc = mma_step<DT>(lds_read16(kb + uint32_t(col * DP * 2 + c * 16)), qf[s], sc);
     }
-    float p[8];
+    if (mask != 0xffffu) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) p[t * 4 + i] = sc[t][i] * a.scale_log2;
-    if (mask != 0xffffffffu) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!((mask >> (t * 16 + grp * 4 + i)) & 1u)) p[t * 4 + i] = kNegInf;
+      for (int i = 0; i < 4; ++i)
+        if (!((mask >> (grp * 4 + i)) & 1u)) sc[i] = kNegInf;
     }
-    float mx = p[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) mx = fmaxf(mx, p[i]);
-    mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-    const float mn = fmaxf(m, mx);
-    const float base = mn == kNegInf ? 0.f : mn;  // nothing visible yet: every p is exp2(-inf) = 0
-    const float alpha = __builtin_amdgcn_exp2f(m - base);
-    m = mn;
-    uint32_t pk[4];
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      pk[i] = pack2<DT>(__builtin_amdgcn_exp2f(p[2 * i] - base), __builtin_amdgcn_exp2f(p[2 * i + 1] - base));
-      sum += Traits<DT>::to_f32(uint16_t(pk[i])) + Traits<DT>::to_f32(uint16_t(pk[i] >> 16));
-    }
-    l = l * alpha + sum;
-    const uint4 pf = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-    if (!__all(alpha == 1.f)) {
+    const float mx = max_groups(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]))) * a.scale_log2;
+    const bool lag = mx > m + kLag;
+    if (__any(lag)) {
+      const float mn = lag ? mx : m;
+      const float alpha = mn == kNegInf ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+      l *= alpha;
 #pragma unroll
       for (int t = 0; t < DTILES; ++t) o[t] *= alpha;
+      m = mn;
     }
+    const float base = m == kNegInf ? 0.f : m;  // nothing visible yet: every weight is exp2(-inf) = 0
+    uint32_t pk[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      pk[i] = cvt2<DT>(__builtin_amdgcn_exp2f(fmaf(sc[2 * i], a.scale_log2, -base)),
+                       __builtin_amdgcn_exp2f(fmaf(sc[2 * i + 1], a.scale_log2, -base)));
+      l = add2<DT>(pk[i], l);
+    }
+    const int r = grp * 4 + (col >> 2), sub = (col & 1) * 8;
 #pragma unroll
     for (int t = 0; t < DTILES; ++t) {
-      const int r0 = grp * 4 + (col >> 2), r1 = r0 + 16;
-      const int c = t * 2 + ((col & 3) >> 1), sub = (col & 1) * 8;
-      const int c0 = c ^ ((r0 & 7) << 1 & (CPR - 1)), c1 = c ^ ((r1 & 7) << 1 & (CPR - 1));
-      const s16x4_t v0 = lds_read_tr(vb + uint32_t(r0 * DP * 2 + c0 * 16 + sub));
-      const s16x4_t v1 = lds_read_tr(vb + uint32_t(r1 * DP * 2 + c1 * 16 + sub));
-      const uint2 u0 = __builtin_bit_cast(uint2, v0), u1 = __builtin_bit_cast(uint2, v1);
-      o[t] = mma_step<DT>(make_uint4(u0.x, u0.y, u1.x, u1.y), pf, o[t]);
+      const int c = (t * 2 + ((col & 3) >> 1)) ^ (((r & 7) << 1) & (CPR - 1));
+      const uint2 v = __builtin_bit_cast(uint2, lds_read_tr(vb + uint32_t(r * DP * 2 + c * 16 + sub)));
+      o[t] = mma16<DT>(v, make_uint2(pk[0], pk[1]), o[t]);
     }
-    // this block's LDS reads are done before the next iteration's loads may overwrite the buffer
+    // this block's LDS reads are done before a later load may overwrite the buffer
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  };
+
+#pragma unroll
+  for (int j = 0; j < NB - 1; ++j)
+    if (j < mine) start(j, masks[j]);
+  for (int j0 = 0; j0 < mine; j0 += NB) {
+#pragma unroll
+    for (int u = 0; u < NB; ++u) {
+      const int j = j0 + u;
+      if (j < mine) {
+        if (j + NB - 1 < mine) {
+          start(j + NB - 1, masks[(u + NB - 1) % NB]);
+          vm_wait<(NB - 1) * 2 * NI>();
+        } else {
+          vm_wait<0>();
+        }
+        asm volatile("" ::: "memory");
+        compute(u, masks[u]);
+      }
+    }
   }
-  l += __shfl_xor(l, 16, 64);
-  l += __shfl_xor(l, 32, 64);
+  l = add_groups(l);
 
   // join the waves: a common maximum, scaled outputs summed through LDS
-  if (grp == 0) s_ml[wave][col] = make_float2(m, l);
+  if (grp == 0) S.ml[wave][col] = make_float2(m, l);
   __syncthreads();
   float mm = kNegInf;
 #pragma unroll
-  for (int x = 0; x < NW; ++x) mm = fmaxf(mm, s_ml[x][col].x);
+  for (int x = 0; x < kWaves; ++x) mm = fmaxf(mm, S.ml[x][col].x);
   const float base = mm == kNegInf ? 0.f : mm;
   float ll = 0.f;
 #pragma unroll
-  for (int x = 0; x < NW; ++x) ll += s_ml[x][col].y * __builtin_amdgcn_exp2f(s_ml[x][col].x - base);
+  for (int x = 0; x < kWaves; ++x) ll += S.ml[x][col].y * __builtin_amdgcn_exp2f(S.ml[x][col].x - base);
   const float f = __builtin_amdgcn_exp2f(m - base);
-  // [16 rows][DP + 4] fp32 per wave, over the wave's own (now idle) buffers
-  float* ob = reinterpret_cast<float*>(&L.kv[0][0][0]);
-  static_assert(sizeof(L.kv) >= sizeof(float) * 16 * (DP + 4), "join buffer");
+  // [16 rows][DP + 4] fp32 per wave, over the wave's own (now idle) buffers and table
+  constexpr int OP = DP + 4;
+  static_assert(sizeof(RowsWave<DP>) >= sizeof(float) * 16 * OP, "join buffer");
+  float* ob = reinterpret_cast<float*>(&L);
+#pragma unroll
+  for (int t = 0; t < DTILES; ++t)
+    *reinterpret_cast<float4*>(ob + col * OP + t * 16 + grp * 4) = make_float4(o[t][0] * f, o[t][1] * f, o[t][2] * f, o[t][3] * f);
+  __syncthreads();
+  const int64_t rows_all = int64_t(a.T) * a.Hq;
+  for (int e = int(threadIdx.x); e < 16 * DP / 4; e += 64 * kWaves) {
+    const int r = e / (DP / 4), d = (e - r * (DP / 4)) * 4;
+    if (r >= w.nrows || d >= a.D) continue;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int x = 0; x < kWaves; ++x) {
+      const float4 u = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(&S.wave[x]) + r * OP + d);
+      v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+    }
+    const int rr = w.row0 + r;
+    const int64_t prow = int64_t(rr / a.grp) * a.Hq + w.kvh * a.grp + rr % a.grp;
+    *reinterpret_cast<float4*>(a.part_o + (int64_t(w.slot) * rows_all + prow) * a.D + d) = v;
+  }
+  if (wave == 0 && grp == 0 && row_ok)
+    a.part_ml[int64_t(w.slot) * rows_all + int64_t(pos) * a.Hq + head] = make_float2(mm, ll);
+}
+
+
+template <int DP>
+constexpr int tile_block() { return DP > 128 ? 32 : 64; }
+
+// Shared prefix tile: 4 waves of 32 query rows each walk the same key blocks, staged once in LDS for
+// all of them (double buffered, one barrier a block).
+template <int DP>
+struct TileLds {
+  uint16_t k[2][tile_block<DP>() * DP];
+  uint16_t v[2][tile_block<DP>() * DP];
+  int64_t off[2][512];
+  uint64_t mask[2][8];
+};
+
+template <int DT, int DP>
+__device__ __forceinline__ void tile_body(const PrefixAttnArgs& a, const Work& w, TileLds<DP>& S) {
+  constexpr int BK = tile_block<DP>();
+  constexpr int CPR = DP / 8, RPI = 64 / CPR;
+  constexpr int NI = BK / RPI / 4;      // DMA instructions per wave, block and operand
+  constexpr int KT = BK / 32, KS = DP / 16, DTILES = DP / 32;
+  constexpr int TB = 512 / BK;          // blocks per half of the offset table
+  const int lane = int(threadIdx.x) & 63, wave = wave_id();
+  const int col = lane & 31, half = lane >> 5;
+  const uint16_t* kc = static_cast<const uint16_t*>(a.k_cache);
+  const uint16_t* vc = static_cast<const uint16_t*>(a.v_cache);
+
+  const int r = wave * 32 + col;
+  const bool row_ok = r < w.nrows;
+  const int row = w.row0 + min(r, w.nrows - 1);
+  const int pos = row / a.grp, head = w.kvh * a.grp + row % a.grp;
+  const int tok = a.permutation != nullptr ? a.permutation[pos] : pos;
+  const bool tok_ok = row_ok && tok >= 0 && tok < a.T;
+  uint4 qf[KS];
+  {
+    const uint16_t* qp = static_cast<const uint16_t*>(a.q) + int64_t(tok_ok ? tok : 0) * a.ldq +
+                         int64_t(head) * a.D;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const int d = s * 16 + half * 8;
+      qf[s] = make_uint4(0u, 0u, 0u, 0u);
+      if (tok_ok && d < a.D) qf[s] = signed_chunk(gload16(qp + d), a.negate);
+    }
+  }
+  f32x16_t o[DTILES];
 #pragma unroll
   for (int t = 0; t < DTILES; ++t)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ob[col * (DP + 4) + t * 16 + grp * 4 + i] = o[t][i] * f;
-  __syncthreads();
-  const int64_t rows_all = int64_t(a.T) * a.Hq;
-  for (int e = int(threadIdx.x); e < 16 * DP; e += 64 * NW) {
-    const int r = e / DP, d = e - r * DP;
-    if (r >= w.nrows || d >= a.D) continue;
-    float v = 0.f;
+    for (int i = 0; i < 16; ++i) o[t][i] = 0.f;
+  float m = kNegInf, l = 0.f;
+  const bool busy = wave * 32 < w.nrows;  // waves without a row only help loading
+
+  const int nblk = (w.k1 - w.k0 + BK - 1) / BK;
+  // Page ids of the 512 keys from table block `first` on: loaded here, two keys a thread, ...
+  auto load_ids = [&](int first, int* id) {
 #pragma unroll
-    for (int x = 0; x < NW; ++x)
-      v += reinterpret_cast<const float*>(&s_wave[x].kv[0][0][0])[r * (DP + 4) + d];
-    const int rr = w.row0 + r;
-    const int64_t prow = int64_t(rr / a.grp) * a.Hq + w.kvh * a.grp + rr % a.grp;
-    a.part_o[(int64_t(w.slot) * rows_all + prow) * a.D + d] = v;
+    for (int e = 0; e < 2; ++e) {
+      const int key = w.k0 + first * BK + e * 256 + int(threadIdx.x);
+      id[e] = key < w.k1 ? w.pages[key / a.page_size] : -1;
+    }
+  };
+  // ... and turned into offsets and masks in half `h` of the table here.
+  auto fill_table = [&](int first, int h, const int* id) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int idx = e * 256 + int(threadIdx.x);
+      const int key = w.k0 + first * BK + idx;
+      const int place = key - key / a.page_size * a.page_size;
+      const bool ok = id[e] >= 0 && id[e] < a.num_pages;
+      S.off[h][idx] = ok ? int64_t(id[e]) * a.page_stride + int64_t(place) * a.token_stride +
+                               int64_t(w.kvh) * a.head_stride
+                         : int64_t(-1);
+      const unsigned long long bits = __ballot(ok);
+      if (lane == 0) S.mask[h][e * 4 + wave] = bits;
+    }
+  };
+  auto issue = [&](int j) {
+    const int buf = j & 1;
+    const int64_t* off = &S.off[(j / TB) & 1][(j % TB) * BK];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int ii = wave * NI + i;
+      const int kr = ii * RPI + lane / CPR;
+      const int64_t of = off[kr];
+      const int cs = lane % CPR;
+      const int ck = cs ^ (kr & (CPR - 1)), cv = cs ^ (((kr & 7) << 1) & (CPR - 1));
+      const bool ok = of >= 0;
+      const void* kp = ok && ck * 8 < a.D ? static_cast<const void*>(kc + of + ck * 8) : &kZeroChunk;
+      const void* vp = ok && cv * 8 < a.D ? static_cast<const void*>(vc + of + cv * 8) : &kZeroChunk;
+      dma16(kp, __builtin_amdgcn_readfirstlane(lds_addr(&S.k[buf][ii * 512])));
+      dma16(vp, __builtin_amdgcn_readfirstlane(lds_addr(&S.v[buf][ii * 512])));
+    }
+  };
+
+  int ids[2];
+  load_ids(0, ids);
+  fill_table(0, 0, ids);
+  __syncthreads();
+  issue(0);
+  for (int j = 0; j < nblk; ++j) {
+    vm_wait<0>();
+    __syncthreads();  // block j is in LDS, and nobody reads the other buffer any more
+    const int ph = j % TB;
+    if (ph == TB - 3 && j + 3 < nblk) load_ids(j + 3, ids);
+    if (j + 1 < nblk) issue(j + 1);
+    if (busy) {
+      const uint32_t kb = lds_addr(&S.k[j & 1][0]), vb = lds_addr(&S.v[j & 1][0]);
+      f32x16_t sc[KT];
+#pragma unroll
+      for (int t = 0; t < KT; ++t) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sc[t][i] = 0.f;
+        const int kr = t * 32 + col;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const int c = (s * 2 + half) ^ (kr & (CPR - 1));
+          sc[t] = mma32<DT>(lds_read16(kb + uint32_t(kr * DP * 2 + c * 16)), qf[s], sc[t]);
+        }
+      }
+      const uint64_t mask = BK == 64 ? S.mask[(j / TB) & 1][ph]
+                                     : (S.mask[(j / TB) & 1][ph / 2] >> (32 * (ph & 1))) & 0xffffffffu;
+      const uint32_t mlo = uniform(int(uint32_t(mask))), mhi = uniform(int(uint32_t(mask >> 32)));
+      if (mlo != 0xffffffffu || (BK == 64 && mhi != 0xffffffffu)) {
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (!(((t ? mhi : mlo) >> (8 * (i / 4) + 4 * half + i % 4)) & 1u)) sc[t][i] = kNegInf;
+      }
+      float mx = sc[0][0];
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, sc[t][i]);
+      mx = max_halves(mx) * a.scale_log2;
+      const bool lag = mx > m + kLag;
+      if (__any(lag)) {
+        const float mn = lag ? mx : m;
+        const float alpha = mn == kNegInf ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+        l *= alpha;
+#pragma unroll
+        for (int t = 0; t < DTILES; ++t) o[t] *= alpha;
+        m = mn;
+      }
+      const float base = m == kNegInf ? 0.f : m;
+      uint4 pf[BK / 16];
+#pragma unroll
+      for (int kk = 0; kk < BK / 16; ++kk) {
+        uint32_t pk[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float s0 = sc[kk / 2][(kk % 2) * 8 + 2 * i], s1 = sc[kk / 2][(kk % 2) * 8 + 2 * i + 1];
+          pk[i] = cvt2<DT>(__builtin_amdgcn_exp2f(fmaf(s0, a.scale_log2, -base)),
+                           __builtin_amdgcn_exp2f(fmaf(s1, a.scale_log2, -base)));
+          l = add2<DT>(pk[i], l);
+        }
+        pf[kk] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+      }
+#pragma unroll
+      for (int kk = 0; kk < BK / 16; ++kk) {
+#pragma unroll
+        for (int t = 0; t < DTILES; ++t) {
+          const int q4 = lane & 15;
+          const int r0 = kk * 16 + half * 4 + (q4 >> 2), r1 = r0 + 8;
+          const int c = t * 4 + ((lane >> 4) & 1) * 2 + ((q4 & 3) >> 1), sub = (q4 & 1) * 8;
+          const int c0 = c ^ (((r0 & 7) << 1) & (CPR - 1)), c1 = c ^ (((r1 & 7) << 1) & (CPR - 1));
+          const uint2 u0 = __builtin_bit_cast(uint2, lds_read_tr(vb + uint32_t(r0 * DP * 2 + c0 * 16 + sub)));
+          const uint2 u1 = __builtin_bit_cast(uint2, lds_read_tr(vb + uint32_t(r1 * DP * 2 + c1 * 16 + sub)));
+          o[t] = mma32<DT>(make_uint4(u0.x, u0.y, u1.x, u1.y), pf[kk], o[t]);
+        }
+      }
+    }
+    if (ph == TB - 3 && j + 3 < nblk) fill_table(j + 3, ((j / TB) & 1) ^ 1, ids);
   }
-  if (wave == 0 && grp == 0 && row_ok) {
-    const int64_t prow = int64_t(pos) * a.Hq + head;
-    a.part_ml[int64_t(w.slot) * rows_all + prow] = make_float2(mm, ll);
-  }
+  l = add_halves(l);
+  if (!row_ok) return;
+  const int64_t rows_all = int64_t(a.T) * a.Hq, prow = int64_t(pos) * a.Hq + head;
+  float* po = a.part_o + (int64_t(w.slot) * rows_all + prow) * a.D;
+#pragma unroll
+  for (int t = 0; t < DTILES; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int d = t * 32 + 8 * (i / 4) + 4 * half;
+      if (d < a.D) *reinterpret_cast<float4*>(po + d) = make_float4(o[t][i], o[t][i + 1], o[t][i + 2], o[t][i + 3]);
+    }
+  if (half == 0) a.part_ml[int64_t(w.slot) * rows_all + prow] = make_float2(m, l);
 }
 
-// Joins the key ranges of every (sorted position, query head): one wave per row.
-template <int DT, int UNIT>
+// One workgroup per (row tile, key head, key range); LDS is whichever layout its tile needs.
+template <int DT, int DP>
+__global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void prefix_attn_kernel(PrefixAttnArgs a) {
+  constexpr size_t kLds = sizeof(TileLds<DP>) > sizeof(RowsLds<DP>) ? sizeof(TileLds<DP>) : sizeof(RowsLds<DP>);
+  __shared__ __align__(16) unsigned char s_mem[kLds];
+  const Work w = find_work(a, int(blockIdx.x));
+  if (!w.live) return;
+  if (w.shared) tile_body<DT, DP>(a, w, *reinterpret_cast<TileLds<DP>*>(s_mem));
+  else rows_body<DT, DP>(a, w, *reinterpret_cast<RowsLds<DP>*>(s_mem));
+}
+
+// Joins the key ranges of every (sorted position, query head): one wave per row. 64 ranges at a
+// time, a lane holds the statistics of one; then 16-byte pieces of the partial rows, as many ranges at
+// once as rows of D fit the wave, four loads in flight.
+template <int DT>
 __global__ __launch_bounds__(256) void prefix_attn_join_kernel(PrefixAttnArgs a) {
   const int64_t row = int64_t(blockIdx.x) * 4 + wave_id();
   const int64_t rows_all = int64_t(a.T) * a.Hq;
@@ -391,36 +675,63 @@ __global__ __launch_bounds__(256) void prefix_attn_join_kernel(PrefixAttnArgs a)
     plen = clamp_len(a.prefix_lens[lo], a.prefix_width, a.page_size);
   }
   if (a.own_splits > 0) olen = clamp_len(a.own_lens[tok], a.own_width, a.page_size);
-  const int slots = a.prefix_splits + a.own_splits;
-  auto used = [&](int s) {
-    int k0, k1;
-    if (s < a.prefix_splits) key_range(plen, a.prefix_splits, s, UNIT, &k0, &k1);
-    else key_range(olen, a.own_splits, s - a.prefix_splits, UNIT, &k0, &k1);
-    return k1 > k0;
-  };
-  float mm = kNegInf;
-  for (int s = 0; s < slots; ++s)
-    if (used(s)) mm = fmaxf(mm, a.part_ml[s * rows_all + row].x);
-  const float base = mm == kNegInf ? 0.f : mm;
-  float ll = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < slots; ++s) {
-    if (!used(s)) continue;
-    const float2 ml = a.part_ml[s * rows_all + row];
-    const float f = __builtin_amdgcn_exp2f(ml.x - base);
-    ll += ml.y * f;
-    const float* po = a.part_o + (s * rows_all + row) * a.D;
+  // the ranges with keys are the first ones of each part
+  const int np = ranges_used(plen, a.prefix_splits, a.prefix_unit);
+  const int n = np + ranges_used(olen, a.own_splits, a.own_unit);
+  auto slot = [&](int s) { return s < np ? s : a.prefix_splits + s - np; };
+
+  const int pieces = a.D / 4, per = pieces > 32 ? 1 : 64 / pieces;  // rows of D a wave loads at once
+  const int sub = lane / pieces, piece = lane - sub * pieces;
+  const bool loads = sub < per;
+  float mm = kNegInf, ll = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < n; s0 += 64) {
+    float2 ml = make_float2(kNegInf, 0.f);
+    if (s0 + lane < n) ml = a.part_ml[slot(s0 + lane) * rows_all + row];
+    float mx = ml.x;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int d = e * 64 + lane;
-      if (d < a.D) acc[e] += po[d] * f;
+    for (int d = 1; d < 64; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d, 64));
+    const float mn = fmaxf(mm, mx), base = mn == kNegInf ? 0.f : mn;
+    const float old = __builtin_amdgcn_exp2f(mm - base);
+    mm = mn;
+    const float f = __builtin_amdgcn_exp2f(ml.x - base);
+    float sum = ml.y * f;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
+    ll = ll * old + sum;
+    acc.x *= old; acc.y *= old; acc.z *= old; acc.w *= old;
+    const int cnt = min(64, n - s0);
+    for (int c = 0; c < cnt; c += 4 * per) {
+      float4 v[4];
+      float g[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int s = c + u * per + sub;
+        const bool ok = loads && s < cnt;
+        g[u] = __shfl(f, s & 63, 64);
+        if (!ok) g[u] = 0.f;
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (ok) v[u] = *reinterpret_cast<const float4*>(a.part_o + (slot(s0 + s) * rows_all + row) * a.D + piece * 4);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        acc.x += v[u].x * g[u]; acc.y += v[u].y * g[u]; acc.z += v[u].z * g[u]; acc.w += v[u].w * g[u];
+      }
     }
+  }
+  // lanes piece, piece + pieces, .. hold shares of the same outputs: added in order into the first
+  float4 tot = acc;
+  for (int s = 1; s < per; ++s) {
+    const int src = (piece + s * pieces) & 63;
+    tot.x += __shfl(acc.x, src, 64); tot.y += __shfl(acc.y, src, 64);
+    tot.z += __shfl(acc.z, src, 64); tot.w += __shfl(acc.w, src, 64);
   }
   const float inv = ll == 0.f ? 0.f : 1.f / ll;  // no visible key: zeros (a NaN sum stays NaN)
   uint16_t* op = static_cast<uint16_t*>(a.out) + int64_t(tok) * a.ldo + int64_t(h) * a.D;
+  if (lane < pieces) {
+    const float r[4] = {tot.x * inv, tot.y * inv, tot.z * inv, tot.w * inv};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int d = e * 64 + lane;
-    if (d < a.D) op[d] = Traits<DT>::from_f32(acc[e] * inv);
+    for (int e = 0; e < 4; ++e) op[lane * 4 + e] = Traits<DT>::from_f32(r[e]);
   }
   if (a.lse != nullptr && lane == 0)
     a.lse[int64_t(tok) * a.Hq + h] = ll == 0.f ? kNegInf : (mm + __log2f(ll)) * 0.6931471805599453f;
@@ -430,13 +741,12 @@ int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 template <int DT, int DP>
 hipError_t launch_dp(const PrefixAttnArgs& a, hipStream_t st) {
-  constexpr int NW = attn_waves<DP>();
   const int64_t grid = int64_t(a.Hkv) * (int64_t(a.prefix_tiles) * a.prefix_splits +
                                          int64_t(a.T) * a.own_tiles * a.own_splits);
   if (grid > 0)
-    hipLaunchKernelGGL((prefix_attn_kernel<DT, DP>), dim3(unsigned(grid)), dim3(64 * NW), 0, st, a);
-  hipLaunchKernelGGL((prefix_attn_join_kernel<DT, kBlk * NW>),
-                     dim3(unsigned(cdiv64(int64_t(a.T) * a.Hq, 4))), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((prefix_attn_kernel<DT, DP>), dim3(unsigned(grid)), dim3(64 * kWaves), 0, st, a);
+  hipLaunchKernelGGL((prefix_attn_join_kernel<DT>), dim3(unsigned(cdiv64(int64_t(a.T) * a.Hq, 4))),
+                     dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
@@ -448,16 +758,21 @@ PrefixAttnPlan prefix_attention_plan(int64_t T, int G, int Hq, int Hkv, int D, i
   p.dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
   const int grp = Hq / Hkv;
   const int64_t pmax = prefix_width * page_size, omax = own_width * page_size;
-  // enough key ranges for about 1024 workgroups, none shorter than 256 keys
-  p.prefix_tiles = int(cdiv64(T * grp, 16) + G);
-  p.own_tiles = int(cdiv64(grp, 16));
-  auto splits = [](int64_t keys, int64_t wgs) {
+  p.shared = T * grp > 32 * int64_t(G);
+  const int tile = p.shared ? kTileRows : kRows;
+  p.prefix_tiles = int(cdiv64(T * grp, tile) + G);
+  p.own_tiles = int(cdiv64(grp, kRows));
+  p.own_unit = 16 * kWaves;
+  p.prefix_unit = p.shared ? (p.dp > 128 ? tile_block<256>() : tile_block<128>()) : p.own_unit;
+  // key ranges for about `target` workgroups, none shorter than `least` keys
+  auto splits = [](int64_t keys, int64_t wgs, int64_t target, int64_t least) {
     if (keys <= 0) return int64_t(0);
-    const int64_t want = std::max<int64_t>(1, 1024 / std::max<int64_t>(wgs, 1));
-    return std::max<int64_t>(1, std::min(want, cdiv64(keys, 256)));
+    const int64_t want = std::max<int64_t>(1, target / std::max<int64_t>(wgs, 1));
+    return std::max<int64_t>(1, std::min(want, cdiv64(keys, least)));
   };
-  p.prefix_splits = int(splits(pmax, int64_t(p.prefix_tiles) * Hkv));
-  p.own_splits = int(splits(omax, T * p.own_tiles * Hkv));
+  const int64_t ptiles = std::max<int64_t>(1, cdiv64(T * grp, tile));
+  p.prefix_splits = int(splits(pmax, ptiles * Hkv, p.shared ? 256 : 1024, 256));
+  p.own_splits = int(splits(omax, T * p.own_tiles * Hkv, 1024, 256));
   const int64_t rows = T * Hq, slots = p.prefix_splits + p.own_splits;
   p.part_ml = size_t(slots * rows * D * 4 + 255) & ~size_t(255);
   p.total = p.part_ml + size_t(slots * rows * 8);

@@ -24,14 +24,18 @@ struct PrefixAttnArgs {
   int T, G, Hq, Hkv, grp, D, page_size, num_pages, prefix_width, own_width;
   int prefix_tiles, prefix_splits;  // row-tile bound and key ranges of the prefix part
   int own_tiles, own_splits;        // row tiles per token and key ranges of the own part
-  float scale_log2;                 // scale * log2(e)
+  int prefix_unit, own_unit;        // keys that a range is a multiple of
+  int shared;                       // prefix tiles of 128 rows, else 16
+  int negate;                       // scale < 0: the queries' signs are flipped
+  float scale_log2;                 // |scale| * log2(e), above 0
 };
 
 // Launch plan from host-known sizes only (lengths live on the device; the page lists' widths bound
 // them).
 struct PrefixAttnPlan {
   int dp;  // head size rounded up to 64, 128 or 256
-  int prefix_tiles, prefix_splits, own_tiles, own_splits;
+  bool shared;  // prefix tiles of 128 rows sharing their key blocks (else 16 rows)
+  int prefix_tiles, prefix_splits, prefix_unit, own_tiles, own_splits, own_unit;
   size_t part_ml, total;  // workspace: byte offset of part_ml, total bytes
 };
 PrefixAttnPlan prefix_attention_plan(int64_t T, int G, int Hq, int Hkv, int D, int page_size,
