@@ -4,7 +4,7 @@ addresses that are never used, and the tensor wrappers."""
 import pytest
 import torch
 
-from adapter_lora_projection_amd import _lib, decode_ops as d, ops
+from adapter_lora_projection_amd import _lib, decode_ops as d
 
 bf = torch.bfloat16
 OK, EINVAL, EUNSUP, EWS = _lib.LORA_OK, _lib.LORA_EINVAL, _lib.LORA_EUNSUPPORTED, _lib.LORA_EWORKSPACE
@@ -115,7 +115,7 @@ def test_attention_workspace_query():
 
 @pytest.fixture
 def no_device_check(monkeypatch):
-    monkeypatch.setattr(ops, "_dev", lambda *ts: None)
+    monkeypatch.setattr(d, "_place", lambda *ts: 0)
 
 
 def test_cpu_tensors_are_refused():
@@ -206,6 +206,7 @@ def test_attention_wrapper(no_device_check, kw):
 
 
 def test_short_workspace_is_refused_by_the_library(no_device_check, monkeypatch):
-    monkeypatch.setattr(d, "_stream", lambda dev: None)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: None, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     with pytest.raises(_lib.LoraError, match="WORKSPACE"):
         d.prefix_attention(**_attn_tensors(workspace=torch.zeros(16, dtype=torch.uint8)))
