@@ -209,6 +209,11 @@ lora_status lora_prefix_attention(lora_dtype dtype, int64_t T, int32_t G, int32_
   a.prefix_width = int(prefix_width); a.own_width = int(own_width);
   a.prefix_tiles = p.prefix_tiles; a.prefix_splits = p.prefix_splits;
   a.own_tiles = p.own_tiles; a.own_splits = p.own_splits;
+  a.by_kvh = lmx::FastDiv::of(Hkv); a.by_grp = lmx::FastDiv::of(a.grp);
+  a.by_page = lmx::FastDiv::of(page_size); a.by_hq = lmx::FastDiv::of(Hq);
+  a.by_prefix_splits = lmx::FastDiv::of(p.prefix_splits);
+  a.by_own_tiles = lmx::FastDiv::of(p.own_tiles); a.by_own_splits = lmx::FastDiv::of(p.own_splits);
+  a.out8 = (reinterpret_cast<uintptr_t>(out) & 7u) == 0 && ldo % 4 == 0;
   a.shared = p.shared; a.prefix_unit = p.prefix_unit; a.own_unit = p.own_unit;
   // the kernels multiply masked scores (-inf) by it: above 0, with the sign in the queries (a scale of
   // 0 gives equal weights, and so does 2^-100)

@@ -6,6 +6,29 @@
 
 namespace lmx {
 
+// n / d for 0 <= n < 2^31 as one high product: m = floor(2^(32 + s) / d) + 1 with s = floor(log2 d) is off
+// by at most d <= 2^(s + 1) parts in 2^(32 + s), which n does not carry over. m = 0 stands for d = 1; a
+// power of two takes 2^31 and one shift less.
+struct FastDiv {
+  uint32_t m, s;
+  int d;
+  static FastDiv of(int64_t d) {
+    FastDiv f{0u, 0u, int(d)};
+    if (d <= 1) return f;
+    while ((int64_t(2) << f.s) <= d) ++f.s;
+    if ((int64_t(1) << f.s) == d) {
+      f.m = 0x80000000u;
+      f.s -= 1;
+    } else {
+      f.m = uint32_t((uint64_t(1) << (32 + f.s)) / uint64_t(d)) + 1u;
+    }
+    return f;
+  }
+  __host__ __device__ int div(int n) const {
+    return m == 0 ? n : int(uint32_t((uint64_t(uint32_t(n)) * m) >> 32) >> s);
+  }
+};
+
 struct PrefixAttnArgs {
   const void* q;        // [T][ldq], head h of token t at t * ldq + h * D
   const void* k_cache;  // element (page, place, head, d) at page * page_stride + place *
@@ -22,10 +45,12 @@ struct PrefixAttnArgs {
   float2* part_ml;          // [slots][T * Hq]: running maximum (base 2) and sum of each
   int64_t ldq, ldo, page_stride, token_stride, head_stride;
   int T, G, Hq, Hkv, grp, D, page_size, num_pages, prefix_width, own_width;
+  FastDiv by_kvh, by_grp, by_page, by_prefix_splits, by_own_tiles, by_own_splits, by_hq;
   int prefix_tiles, prefix_splits;  // row-tile bound and key ranges of the prefix part
   int own_tiles, own_splits;        // row tiles per token and key ranges of the own part
   int prefix_unit, own_unit;        // keys that a range is a multiple of
   int shared;                       // prefix tiles of 128 rows, else 16
+  int out8;                         // output rows are 8-byte aligned
   int negate;                       // scale < 0: the queries' signs are flipped
   float scale_log2;                 // |scale| * log2(e), above 0
 };
