@@ -564,36 +564,41 @@ __device__ __forceinline__ void tile_body(const PrefixAttnArgs& a, const Work& w
       if (lane == 0) S.mask[h][e * 4 + wave] = bits;
     }
   };
+  const int lrow = wave * RPI + lane / CPR, cs = lane % CPR;
+  // Mask and offsets of the next block to load, read from LDS a block ahead of their use.
+  int64_t off[NI];
+  uint64_t raw_mask;
+  auto look_up = [&](int j) {
+    raw_mask = S.mask[(j / TB) & 1][j % TB * BK / 64];
+    const int64_t* t = &S.off[(j / TB) & 1][(j % TB) * BK + lrow];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) off[i] = t[i * 4 * RPI];
+  };
   auto block_mask = [&](int j) {
-    const uint64_t v = S.mask[(j / TB) & 1][j % TB * BK / 64];
-    const uint32_t lo = uint32_t(uniform(int(uint32_t(v)))), hi = uint32_t(uniform(int(uint32_t(v >> 32))));
+    const uint32_t lo = uint32_t(uniform(int(uint32_t(raw_mask)))), hi = uint32_t(uniform(int(uint32_t(raw_mask >> 32))));
     if constexpr (BK == 64) return uint64_t(lo) | (uint64_t(hi) << 32);
     else return uint64_t((j & 1) ? hi : lo);
   };
   constexpr uint64_t kFull = BK == 64 ? ~uint64_t(0) : uint64_t(0xffffffffu);
 
-  const int lrow = wave * RPI + lane / CPR, cs = lane % CPR;
   const int ck = cs ^ (lrow & KM), cv = cs ^ (((lrow & 7) << 1) & (CPR - 1));
   const bool k_in = ck * 8 < a.D, v_in = cv * 8 < a.D, whole = a.D == DP;
   const char* kbase = static_cast<const char*>(a.k_cache) + ck * 16;
   const char* vbase = static_cast<const char*>(a.v_cache) + cv * 16;
   const uint32_t lds0 = uint32_t(uniform(int(lds_addr(&S.kv[0][0][0])))) + wave * 1024;
-  auto issue = [&](int j, uint64_t mask, auto buf) {
-    const int64_t* off = &S.off[(j / TB) & 1][(j % TB) * BK + lrow];
+  auto issue = [&](uint64_t mask, auto buf) {
     constexpr uint32_t kOff = buf.value * 2 * BB, vOff = kOff + BB;
     if (whole && mask == kFull) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int64_t of = off[i * 4 * RPI];
-        dma16(kbase + of, lds0 + kOff + i * 4096);
-        dma16(vbase + of, lds0 + vOff + i * 4096);
+        dma16(kbase + off[i], lds0 + kOff + i * 4096);
+        dma16(vbase + off[i], lds0 + vOff + i * 4096);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int64_t of = off[i * 4 * RPI];
-        const void* kp = of >= 0 && k_in ? static_cast<const void*>(kbase + of) : &kZeroChunk;
-        const void* vp = of >= 0 && v_in ? static_cast<const void*>(vbase + of) : &kZeroChunk;
+        const void* kp = off[i] >= 0 && k_in ? static_cast<const void*>(kbase + off[i]) : &kZeroChunk;
+        const void* vp = off[i] >= 0 && v_in ? static_cast<const void*>(vbase + off[i]) : &kZeroChunk;
         dma16(kp, lds0 + kOff + i * 4096);
         dma16(vp, lds0 + vOff + i * 4096);
       }
@@ -601,60 +606,55 @@ __device__ __forceinline__ void tile_body(const PrefixAttnArgs& a, const Work& w
   };
 
   // Lane addresses of the fragments: K row col, chunk 2 s + half; V row 4 half + q4 / 4 of 16 keys, the
-  // 4 columns of q4 % 4 in the 16 of this lane group.
-  lds_byte* lds = (lds_byte*)(&S.kv[0][0][0]);
-  lds_byte* kaddr[KS];
-#pragma unroll
-  for (int s = 0; s < KS; ++s) kaddr[s] = lds + col * DP * 2 + ((s * 2 + half) ^ (col & KM)) * 16;
-  lds_byte* vaddr[DTILES];
+  // 4 columns of q4 % 4 in the 16 of this lane group of 32-column tile t. The swizzle is an XOR, and so
+  // is the step s or t: one address each, as the LDS is aligned beyond a row.
+  const uint32_t lds = uint32_t(uniform(int(lds_addr(&S.kv[0][0][0]))));
+  const uint32_t kaddr = lds + col * DP * 2 + (half ^ (col & KM)) * 16;
+  uint32_t vaddr;
   {
     const int q4 = lane & 15, vr = half * 4 + (q4 >> 2);
-#pragma unroll
-    for (int t = 0; t < DTILES; ++t) {
-      const int c = t * 4 + ((lane >> 4) & 1) * 2 + ((q4 & 3) >> 1);
-      vaddr[t] = lds + vr * DP * 2 + (c ^ (((vr & 7) << 1) & (CPR - 1))) * 16 + (q4 & 1) * 8;
-    }
+    const int c = ((lane >> 4) & 1) * 2 + ((q4 & 3) >> 1);
+    vaddr = lds + vr * DP * 2 + (c ^ (((vr & 7) << 1) & (CPR - 1))) * 16 + (q4 & 1) * 8;
   }
 
+  constexpr int kAhead = 4;  // K steps read ahead
+  uint4 kf[kAhead][KT];
+  auto read_k = [&](auto buf, auto s) {
+    static_for<KT>([&](auto t) {
+      kf[s.value % kAhead][t.value] = tile_read16<buf.value * 2 * BB + t.value * 32 * DP * 2>(reinterpret_cast<lds_byte*>(kaddr ^ (s.value * 32)));
+    });
+  };
   auto compute = [&](uint64_t mask, auto buf) {
-    constexpr int kOff = buf.value * 2 * BB, vOff = kOff + BB;
+    constexpr int vOff = buf.value * 2 * BB + BB;
     f32x16_t sc[KT];
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
       for (int i = 0; i < 16; ++i) sc[t][i] = 0.f;
-    constexpr int SG = KS < 8 ? KS : 8;  // K fragments are read 8 steps at a time
-    static_for<KS / SG>([&](auto g) {
-      uint4 kf[KT][SG];
-      static_for<SG>([&](auto s) {
-        static_for<KT>([&](auto t) {
-          kf[t.value][s.value] = tile_read16<kOff + t.value * 32 * DP * 2>(kaddr[g.value * SG + s.value]);
-        });
-      });
-      __builtin_amdgcn_sched_barrier(0);
+    static_for<KS>([&](auto s) {
 #pragma unroll
-      for (int s = 0; s < SG; ++s)
-#pragma unroll
-        for (int t = 0; t < KT; ++t) sc[t] = mma32<DT>(kf[t][s], qf[g.value * SG + s], sc[t]);
+      for (int t = 0; t < KT; ++t) sc[t] = mma32<DT>(kf[s.value % kAhead][t], qf[s.value], sc[t]);
+      if constexpr (s.value + kAhead < KS) read_k(buf, std::integral_constant<int, s.value + kAhead>{});
       __builtin_amdgcn_sched_barrier(0);
     });
     // V fragments of the first 32 keys, read under the softmax
     uint4 vf[2][DTILES];
     static_for<2>([&](auto kk) {
       static_for<DTILES>([&](auto t) {
-        const uint2 u0 = tile_read_tr<vOff + kk.value * 16 * DP * 2>(vaddr[t.value]);
-        const uint2 u1 = tile_read_tr<vOff + (kk.value * 16 + 8) * DP * 2>(vaddr[t.value]);
+        const uint2 u0 = tile_read_tr<vOff + kk.value * 16 * DP * 2>(reinterpret_cast<lds_byte*>(vaddr ^ (t.value * 64)));
+        const uint2 u1 = tile_read_tr<vOff + (kk.value * 16 + 8) * DP * 2>(reinterpret_cast<lds_byte*>(vaddr ^ (t.value * 64)));
         vf[kk.value][t.value] = make_uint4(u0.x, u0.y, u1.x, u1.y);
       });
     });
     __builtin_amdgcn_sched_barrier(0);
     if (mask != kFull) {
-      asm volatile("");  // a branch, not 32 selects in every block
 #pragma unroll
-      for (int t = 0; t < KT; ++t)
+      for (int t = 0; t < KT; ++t) {
+        const uint32_t mine = uint32_t(mask >> (32 * t)) >> (4 * half);  // register i: key 8 (i / 4) + 4 half + i % 4
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (!((uint32_t(mask >> (32 * t)) >> (8 * (i / 4) + 4 * half + i % 4)) & 1u)) sc[t][i] = kNegInf;
+          if (!((mine >> (8 * (i / 4) + i % 4)) & 1u)) sc[t][i] = kNegInf;
+      }
     }
     float mx = sc[0][0];
 #pragma unroll
@@ -689,8 +689,8 @@ __device__ __forceinline__ void tile_body(const PrefixAttnArgs& a, const Work& w
       static_for<DTILES>([&](auto t) {
         o[t.value] = mma32<DT>(vf[kk.value & 1][t.value], pf[kk.value], o[t.value]);
         if constexpr (kk.value + 2 < PK) {
-          const uint2 u0 = tile_read_tr<vOff + (kk.value + 2) * 16 * DP * 2>(vaddr[t.value]);
-          const uint2 u1 = tile_read_tr<vOff + ((kk.value + 2) * 16 + 8) * DP * 2>(vaddr[t.value]);
+          const uint2 u0 = tile_read_tr<vOff + (kk.value + 2) * 16 * DP * 2>(reinterpret_cast<lds_byte*>(vaddr ^ (t.value * 64)));
+          const uint2 u1 = tile_read_tr<vOff + ((kk.value + 2) * 16 + 8) * DP * 2>(reinterpret_cast<lds_byte*>(vaddr ^ (t.value * 64)));
           vf[kk.value & 1][t.value] = make_uint4(u0.x, u0.y, u1.x, u1.y);
         }
       });
@@ -701,16 +701,21 @@ __device__ __forceinline__ void tile_body(const PrefixAttnArgs& a, const Work& w
   load_ids(0, ids);
   fill_table(0, 0, ids);
   __syncthreads();
+  look_up(0);
   uint64_t mask = block_mask(0), next = 0;
-  issue(0, mask, std::integral_constant<int, 0>{});
+  issue(mask, std::integral_constant<int, 0>{});
+  look_up(1);
   auto step = [&](int j, auto buf) {
     vm_wait<0>();
     __syncthreads();  // block j is in LDS, and nobody reads the other buffer any more
+    if (busy) static_for<kAhead>([&](auto s) { read_k(buf, s); });
+    __builtin_amdgcn_sched_barrier(0);
     const bool refill = j % TB == TB - 3 && j + 3 < nblk;
     if (refill) load_ids(j + 3, ids);
     if (j + 1 < nblk) {
       next = block_mask(j + 1);
-      issue(j + 1, next, std::integral_constant<int, 1 - buf.value>{});
+      issue(next, std::integral_constant<int, 1 - buf.value>{});
+      look_up(j + 2);  // not used beyond the last block
     }
     if (busy) compute(mask, buf);
     if (refill) fill_table(j + 3, ((j / TB) & 1) ^ 1, ids);
@@ -738,7 +743,7 @@ __device__ __forceinline__ void tile_body(const PrefixAttnArgs& a, const Work& w
 template <int DT, int DP>
 __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void prefix_attn_kernel(PrefixAttnArgs a) {
   constexpr size_t kLds = sizeof(TileLds<DP>) > sizeof(RowsLds<DP>) ? sizeof(TileLds<DP>) : sizeof(RowsLds<DP>);
-  __shared__ __align__(16) unsigned char s_mem[kLds];
+  __shared__ __align__(1024) unsigned char s_mem[kLds];
   const Work w = find_work(a, int(blockIdx.x));
   if (w.k1 <= w.k0) {  // no keys in this range: its rows say so to the join
     const int64_t rows_all = int64_t(a.T) * a.Hq;
