@@ -1,7 +1,8 @@
 """Build the HIP library for gfx950 in-tree: ``python -m adapter_lora_projection_amd.build``.
 
 Compiles every ``csrc/*.hip`` source with hipcc (one object per source, in parallel) and links
-``liblora_mi355x.so`` next to this file. Always rebuilds.
+``liblora_mi355x.so`` next to this file, then ``_binding.so``, the native tensor marshalling of the
+decode-step operators (``csrc/binding.cpp``, against that library and torch). Always rebuilds.
 """
 
 from __future__ import annotations
@@ -15,6 +16,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "liblora_mi355x.so")
+BINDING = os.path.join(HERE, "_binding.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 ARCH = "gfx950"
 
@@ -43,10 +45,40 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_binding() -> str:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    obj = os.path.join(BUILD_DIR, "binding.cpp.o")
+    system = [*cpp_extension.include_paths(), "/opt/rocm/include", sysconfig.get_paths()["include"]]
+    _run([hipcc(), "-x", "c++", "-O2", "-std=c++20", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          *[f for d in system for f in ("-isystem", d)], "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj])
+    return obj
+
+
+def _run(cmd: list[str]) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    _run([hipcc(), "-shared", "-fPIC", "-o", BINDING + ".tmp", obj, f"-L{HERE}", "-l:" + os.path.basename(OUT),
+          f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10_hip", "-lc10", "-Wl,-rpath,$ORIGIN"])
+    os.replace(BINDING + ".tmp", BINDING)
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".hip"))
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, srcs))
     tmp = OUT + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
@@ -54,8 +86,9 @@ def build(verbose: bool = True) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, OUT)
+    _link_binding(binding.result())
     if verbose:
-        print(f"built {OUT} from {len(srcs)} sources", file=sys.stderr)
+        print(f"built {OUT} from {len(srcs)} sources, and {BINDING}", file=sys.stderr)
     return OUT
 
 

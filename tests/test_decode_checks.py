@@ -4,7 +4,7 @@ addresses that are never used, and the tensor wrappers."""
 import pytest
 import torch
 
-from adapter_lora_projection_amd import _lib, decode_ops as d
+from adapter_lora_projection_amd import _lib, decode_ops as d, ops
 
 bf = torch.bfloat16
 OK, EINVAL, EUNSUP, EWS = _lib.LORA_OK, _lib.LORA_EINVAL, _lib.LORA_EUNSUPPORTED, _lib.LORA_EWORKSPACE
@@ -115,7 +115,15 @@ def test_attention_workspace_query():
 
 @pytest.fixture
 def no_device_check(monkeypatch):
-    monkeypatch.setattr(d, "_place", lambda *ts: 0)
+    monkeypatch.setattr(ops, "_dev", lambda *ts: None)
+
+
+def _refused(call, kinds=(ValueError, TypeError)):
+    """The call is refused for its own fault: the check of the device is the last one, so CPU tensors
+    stand in for device ones."""
+    with pytest.raises(kinds) as e:
+        call()
+    assert "GPU" not in str(e.value), e.value
 
 
 def test_cpu_tensors_are_refused():
@@ -123,7 +131,7 @@ def test_cpu_tensors_are_refused():
     with pytest.raises(ValueError, match="GPU"):
         d.linear_w4_prepare(torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(4, 1, dtype=bf))
     with pytest.raises(ValueError, match="GPU"):
-        d.linear_w4(z, d.W4Weight(torch.zeros(8, dtype=torch.uint8), bf, 64, 4, 64, False))
+        d.linear_w4(z, d.W4Weight(torch.zeros(2304, dtype=torch.uint8), bf, 64, 4, 64, False))
     with pytest.raises(ValueError, match="GPU"):
         d.rope_append(**_rope_tensors())
     with pytest.raises(ValueError, match="GPU"):
@@ -146,13 +154,16 @@ def test_w4_prepare_wrapper(no_device_check, codes, scales, zp):
         d.linear_w4_prepare(codes, scales, zp)
 
 
-def test_w4_wrapper(no_device_check):
-    w = d.W4Weight(torch.zeros(8, dtype=torch.uint8), bf, 64, 4, 64, False)
+def test_w4_wrapper():
+    w = d.W4Weight(torch.zeros(2304, dtype=torch.uint8), bf, 64, 4, 64, False)
+    _refused(lambda: d.linear_w4(torch.zeros(2, 64, dtype=bf), d.W4Weight(w.data[:1024], bf, 64, 4, 64, False)))
     for x, out in ((torch.zeros(2, 64), None), (torch.zeros(2, 32, dtype=bf), None),
                    (torch.zeros(64, 2, dtype=bf).t(), None), (torch.zeros(2, 64, dtype=bf), torch.zeros(2, 5, dtype=bf)),
                    (torch.zeros(2, 64, dtype=bf), torch.zeros(2, 4))):
-        with pytest.raises((ValueError, TypeError)):
-            d.linear_w4(x, w, out)
+        _refused(lambda: d.linear_w4(x, w, out))
+    w = d.W4Weight(torch.zeros(2304, dtype=torch.uint8), bf, 64, 4, 64, False)
+    with pytest.raises(ValueError, match="GPU"):  # sizes right, nothing left but the device
+        d.linear_w4(torch.zeros(2, 64, dtype=bf), w)
 
 
 def _rope_tensors(**kw):
@@ -175,9 +186,8 @@ def _rope_tensors(**kw):
     dict(q_norm=torch.zeros(63, dtype=bf)), dict(k_norm=torch.zeros(64)), dict(q_out=torch.zeros(3, 64, dtype=bf)),
     dict(q_out=torch.zeros(3, 128)),
 ])
-def test_rope_wrapper(no_device_check, kw):
-    with pytest.raises((ValueError, TypeError)):
-        d.rope_append(**_rope_tensors(**kw))
+def test_rope_wrapper(kw):
+    _refused(lambda: d.rope_append(**_rope_tensors(**kw)))
 
 
 def _attn_tensors(**kw):
@@ -200,13 +210,15 @@ def _attn_tensors(**kw):
     dict(own_pages=torch.zeros(2, 3, dtype=torch.int32).t()), dict(own_lens=None), dict(out=torch.zeros(3, 64, dtype=bf)),
     dict(out=torch.zeros(3, 128)), dict(workspace=torch.zeros(4)),
 ])
-def test_attention_wrapper(no_device_check, kw):
-    with pytest.raises((ValueError, TypeError)):
-        d.prefix_attention(**_attn_tensors(**kw))
+def test_attention_wrapper(kw):
+    _refused(lambda: d.prefix_attention(**_attn_tensors(**kw)))
 
 
-def test_short_workspace_is_refused_by_the_library(no_device_check, monkeypatch):
-    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: None, raising=False)
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+@pytest.mark.parametrize("kw", [dict(q="x"), dict(k_cache=None), dict(scale="x"), dict(own_pages=3)])
+def test_attention_wrapper_types(kw):
+    _refused(lambda: d.prefix_attention(**_attn_tensors(**kw)), TypeError)
+
+
+def test_status_becomes_an_error():
     with pytest.raises(_lib.LoraError, match="WORKSPACE"):
-        d.prefix_attention(**_attn_tensors(workspace=torch.zeros(16, dtype=torch.uint8)))
+        d._result("lora_prefix_attention", EWS)

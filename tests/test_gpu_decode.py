@@ -272,6 +272,31 @@ def test_attention_without_prefixes_or_own_keys():
         assert drop == "both" or not np.array_equal(f64(out), both)
 
 
+def test_refusals_of_the_library_on_the_gpu():
+    """What only the library can refuse raises before anything is written."""
+    c = dc.Attn(8, "bf16", 5, [3, 2], 4, 2, 64, 16, [40, 70], [5, 6, 7, 30, 0])
+    out = torch.full((5, 256), 7.0, dtype=DT["bf16"], device="cuda")
+    err = lm.LoraError
+    with pytest.raises(err, match="WORKSPACE"):
+        lm.prefix_attention(*c.args(dev), out=out, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    a = list(c.args(dev))
+    with pytest.raises(err, match="UNSUPPORTED"):  # rows of q off the 16-byte grid
+        lm.prefix_attention(torch.zeros((5, 260), dtype=DT["bf16"], device="cuda")[:, 2:258], *a[1:], out=out)
+    with pytest.raises(err, match="EINVAL"):
+        lm.prefix_attention(*a[:9], float("nan"), out=out)
+    with pytest.raises(ValueError, match="GPU"):
+        lm.prefix_attention(c.q, *a[1:], out=out)
+    k = a[1].expand(a[1].shape)
+    with pytest.raises(err, match="EINVAL"):  # places that overlap
+        lm.rope_append(a[0], a[0][:, :128], a[0][:, :128], dev(dc.table(4, 64)), dev(torch.zeros(5, dtype=torch.int32)),
+                       dev(torch.arange(5)), k[:1].expand(4, -1, -1, -1), k[:1].expand(4, -1, -1, -1))
+    w = lm.linear_w4_prepare(torch.zeros((16, 32), dtype=torch.uint8, device="cuda"), torch.ones((16, 1), dtype=DT["f16"], device="cuda"))
+    with pytest.raises(err, match="UNSUPPORTED"):
+        lm.linear_w4(torch.zeros((2, 66), dtype=DT["f16"], device="cuda")[:, 1:65], w)
+    torch.cuda.synchronize()
+    assert torch.all(out == 7.0)
+
+
 def test_attention_same_sequence_several_tokens():
     """Tokens of one sequence as rows that repeat its pages with lengths rising by one."""
     c = dc.Attn(9, "bf16", 6, [6], 8, 2, 128, 16, [100], [37] * 6)
