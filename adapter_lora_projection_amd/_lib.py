@@ -91,7 +91,9 @@ SIGNATURES = {
     "lora_linear_w4_prepared_size": (_sz, [_i32, _i64, _i64, _i32, _i32]),
     "lora_linear_w4_prepare": (_i32, [_i32, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
                                       _sz, _vp]),
-    "lora_linear_w4": (_i32, [_i32, _i64, _i64, _i64, _i32, _i32, _vp, _i64, _vp, _vp, _i64, _vp]),
+    "lora_linear_w4": (_i32, [_i32, _i64, _i64, _i64, _i32, _i32, _vp, _i64, _vp, _vp, _i64, _vp, _sz,
+                              _vp]),
+    "lora_linear_w4_workspace_size": (_sz, [_i32, _i64, _i64, _i64, _i32]),
     "lora_rope_append": (_i32, [_i32, _i64, _i32, _i32, _i32, _i32, _i32, _i64, _i32, _i64, _vp,
                                 _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp,
                                 ctypes.c_float, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _vp]),
@@ -383,10 +385,15 @@ def lora_linear_w4_prepare(dtype, K, N, group, codes, ldc, scales, lds, zero_poi
     _check("lora_linear_w4_prepare", st)
 
 
-def lora_linear_w4(dtype, M, K, N, group, zero_points, x, ldx, prepared, y, ldy, stream) -> None:
+def lora_linear_w4(dtype, M, K, N, group, zero_points, x, ldx, prepared, y, ldy, workspace,
+                   workspace_bytes, stream) -> None:
     st = lib().lora_linear_w4(dtype, M, K, N, group, zero_points, _p(x), ldx, _p(prepared), _p(y),
-                              ldy, stream)
+                              ldy, _p(workspace), workspace_bytes, stream)
     _check("lora_linear_w4", st)
+
+
+def lora_linear_w4_workspace_size(dtype, M, K, N, group) -> int:
+    return int(lib().lora_linear_w4_workspace_size(dtype, M, K, N, group))
 
 
 def lora_rope_append(dtype, T, Hq, Hkv, D, rot, interleaved, num_pages, page_size, table_rows, q,

@@ -77,9 +77,15 @@ lora_status lora_linear_w4_prepare(lora_dtype dtype, int64_t K, int64_t N, int32
   return hip_status(lmx::launch_w4_prepare(a, reinterpret_cast<hipStream_t>(stream)));
 }
 
+size_t lora_linear_w4_workspace_size(lora_dtype dtype, int64_t M, int64_t K, int64_t N, int32_t group) {
+  if (w4_sizes(dtype, K, N, group) != LORA_OK || M < 1 || M > (int64_t(1) << 20)) return 0;
+  return lmx::w4_plan(M, K, N, group).workspace;
+}
+
 lora_status lora_linear_w4(lora_dtype dtype, int64_t M, int64_t K, int64_t N, int32_t group,
                            int32_t zero_points, const void* x, int64_t ldx, const void* prepared,
-                           void* y, int64_t ldy, void* stream) {
+                           void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                           void* stream) {
   const lora_status st = w4_sizes(dtype, K, N, group);
   if (st != LORA_OK) return st;
   if (M < 0) return LORA_EINVAL;
@@ -87,12 +93,16 @@ lora_status lora_linear_w4(lora_dtype dtype, int64_t M, int64_t K, int64_t N, in
   if (M == 0) return LORA_OK;
   if (!x || !prepared || !y || ldx < K || ldy < N) return LORA_EINVAL;
   if (!al16(x) || ldx % 8 != 0 || !al16(prepared)) return LORA_EUNSUPPORTED;
+  const lmx::W4Plan p = lmx::w4_plan(M, K, N, group);
+  if (p.workspace > 0 && (workspace == nullptr || workspace_bytes < p.workspace || !al16(workspace)))
+    return LORA_EWORKSPACE;
   lmx::W4Args a{};
+  a.part = static_cast<float*>(workspace);
   a.x = static_cast<const uint16_t*>(x); a.w = static_cast<const uint8_t*>(prepared);
   a.y = static_cast<uint16_t*>(y);
   a.ldx = ldx; a.ldy = ldy;
   a.M = int(M); a.K = int(K); a.N = int(N); a.group = group;
-  return hip_status(lmx::launch_linear_w4(a, dtype, zero_points != 0, reinterpret_cast<hipStream_t>(stream)));
+  return hip_status(lmx::launch_linear_w4(a, p, dtype, zero_points != 0, reinterpret_cast<hipStream_t>(stream)));
 }
 
 lora_status lora_rope_append(lora_dtype dtype, int64_t T, int32_t Hq, int32_t Hkv, int32_t D,

@@ -167,8 +167,12 @@ PyObject* linear_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int dev = device_of({&x, &data, given});
     const at::Tensor out = output(given, x.size(0), N, x, "out");
     const int64_t ldy = pitch(out, "out");
+    const size_t bytes = lora_linear_w4_workspace_size(dt, x.size(0), K, N, group);
+    at::Tensor ws;
+    if (bytes > 0) ws = at::empty({int64_t(bytes)}, x.options().dtype(at::kByte));
     const lora_status st = launch(dev, [&](void* stream) {
-      return lora_linear_w4(dt, x.size(0), K, N, group, zp, x.data_ptr(), ldx, data.data_ptr(), out.data_ptr(), ldy, stream);
+      return lora_linear_w4(dt, x.size(0), K, N, group, zp, x.data_ptr(), ldx, data.data_ptr(), out.data_ptr(), ldy,
+                            bytes > 0 ? ws.data_ptr() : nullptr, bytes, stream);
     });
     return st == LORA_OK ? THPVariable_Wrap(out) : status(st);
   });

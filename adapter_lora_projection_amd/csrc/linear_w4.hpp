@@ -41,9 +41,18 @@ struct W4Args {
   const uint16_t* x;  // [M][ldx]
   const uint8_t* w;   // prepared
   uint16_t* y;        // [M][ldy]
+  float* part;        // planes of W4Plan
   int64_t ldx, ldy;
   int M, K, N, group;
 };
-hipError_t launch_linear_w4(const W4Args& a, int dtype, bool zeros, hipStream_t st);
+// How a product is shared out, from its sizes alone.
+struct W4Plan {
+  int ranges;        // 0: column kernel; else slab kernel over this many ranges of K
+  bool wide;         // column kernel with 16 waves (else 8)
+  size_t workspace;  // bytes: fp32 planes [ranges][M][ceil(N / 16) * 16] of more than one range
+};
+W4Plan w4_plan(int64_t M, int64_t K, int64_t N, int group);
+
+hipError_t launch_linear_w4(const W4Args& a, const W4Plan& p, int dtype, bool zeros, hipStream_t st);
 
 }  // namespace lmx

@@ -582,10 +582,12 @@ lora_status lora_embedding_a(lora_dtype dtype, int64_t T, int64_t V, int32_t R, 
  *                  not needed afterwards.
  * lora_linear_w4 takes the same dtype, K, N, group and presence of zero points, and
  *   x [M][ldx >= K], 16-byte aligned rows; y [M][ldy >= N], any alignment (not accumulated into; must
- *   not overlap x). No workspace, one launch.
+ *   not overlap x); workspace: device scratch of lora_linear_w4_workspace_size(...) bytes (partial
+ *   sums of ranges of K; 0 for one or two rows, and wherever one launch is faster), 16-byte aligned, not
+ *   read before written. Calls that overlap in time must not share it.
  * Errors: LORA_EUNSUPPORTED (dtype, group, K or N above 2^24, M above 2^20, unaligned x or
- * prepared), LORA_EINVAL (sizes, K % group, pitches, null pointers), LORA_EWORKSPACE (prepared too
- * small), LORA_EHIP. lora_linear_w4_prepared_size returns 0 for sizes that are refused.
+ * prepared), LORA_EINVAL (sizes, K % group, pitches, null pointers), LORA_EWORKSPACE (prepared or
+ * workspace too small or unaligned), LORA_EHIP. lora_linear_w4_prepared_size returns 0 for sizes that are refused.
  */
 lora_status lora_linear_w4_prepare(lora_dtype dtype, int64_t K, int64_t N, int32_t group,
                                    const uint8_t* codes, int64_t ldc, const void* scales,
@@ -597,7 +599,11 @@ size_t lora_linear_w4_prepared_size(lora_dtype dtype, int64_t K, int64_t N, int3
 
 lora_status lora_linear_w4(lora_dtype dtype, int64_t M, int64_t K, int64_t N, int32_t group,
                            int32_t zero_points, const void* x, int64_t ldx, const void* prepared,
-                           void* y, int64_t ldy, void* stream);
+                           void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+size_t lora_linear_w4_workspace_size(lora_dtype dtype, int64_t M, int64_t K, int64_t N,
+                                     int32_t group);
 
 /*
  * lora_rope_append -- what follows a q/k/v projection: the rotation of queries and keys (with an

@@ -30,7 +30,8 @@ def test_w4_prepare_refusals(kw, code):
 
 
 def _w4(**kw):
-    a = dict(dtype=1, M=4, K=256, N=32, group=64, zp=0, x=0x1000, ldx=256, w=0x2000, y=0x3000, ldy=32, stream=None)
+    a = dict(dtype=1, M=4, K=256, N=32, group=64, zp=0, x=0x1000, ldx=256, w=0x2000, y=0x3000, ldy=32,
+             ws=None, nbytes=0, stream=None)
     a.update(kw)
     return _lib.lib().lora_linear_w4(*a.values())
 
@@ -40,6 +41,8 @@ def _w4(**kw):
     (dict(group=16), EUNSUP), (dict(x=None), EINVAL), (dict(w=None), EINVAL), (dict(y=None), EINVAL),
     (dict(ldx=255), EINVAL), (dict(ldx=260), EUNSUP), (dict(ldy=31), EINVAL), (dict(x=0x1002), EUNSUP),
     (dict(w=0x2008), EUNSUP), (dict(M=0, x=None, y=None), OK),
+    (dict(M=64, K=8192, N=4096, group=128, ldx=8192, ldy=4096), EWS),  # needs planes
+    (dict(M=64, K=8192, N=4096, group=128, ldx=8192, ldy=4096, ws=0x10008, nbytes=1 << 40), EWS),
 ])
 def test_w4_refusals(kw, code):
     assert _w4(**kw) == code
@@ -52,6 +55,14 @@ def test_w4_prepared_size():
     assert _lib.lora_linear_w4_prepared_size(1, 96, 17, 32, 0) == 2048 + 256  # 192 rounded up to 256
     assert _lib.lora_linear_w4_prepared_size(0, 256, 32, 64, 0) == 0
     assert _lib.lora_linear_w4_prepared_size(1, 250, 32, 64, 0) == 0
+
+
+def test_w4_workspace_size():
+    size = _lib.lora_linear_w4_workspace_size
+    assert size(1, 1, 16384, 28672, 128) == 0 and size(1, 2, 16384, 1024, 128) == 0
+    n = size(1, 64, 8192, 4096, 128)  # planes of [64][4096] floats
+    assert n > 0 and n % (64 * 4096 * 4) == 0
+    assert size(1, 0, 8192, 4096, 128) == 0 and size(1, 64, 8192, 4096, 48) == 0 and size(0, 64, 8192, 4096, 128) == 0
 
 
 def _rope(**kw):

@@ -29,6 +29,9 @@ def _w4(x, codes, scales, zp, **kw):
     (17, 1056, 1000, 32, True), (33, 640, 70, 128, False), (70, 256, 48, 64, True),
     (1, 4096, 512, 128, False), (2, 16384, 64, 64, True), (130, 128, 130, 32, True),
     (8, 4096, 4096, 128, True), (64, 2048, 272, 128, True),
+    # ranges of K in fp32 planes (16, 32 and 64 rows a workgroup), and slabs over all of K
+    (16, 16384, 72, 128, False), (24, 8192, 260, 64, True), (24, 8192, 260, 32, True), (33, 12288, 100, 128, True),
+    (40, 256, 16500, 64, False), (64, 128, 20000, 128, True), (20, 96, 30000, 32, True), (5, 32, 50000, 32, False),
 ])
 def test_w4(dtype, M, K, N, group, zeros):
     print("w4", dtype, M, K, N, group, zeros, flush=True)
@@ -40,25 +43,27 @@ def test_w4(dtype, M, K, N, group, zeros):
     assert torch.equal(y, again)
 
 
-def test_w4_strided_rows_and_output():
-    x, codes, scales, zp = dc.w4_inputs(5, "bf16", 6, 160, 37, 32, True)
-    wide = torch.full((6, 200), float("nan"), dtype=DT["bf16"])
-    wide[:, :160] = x
-    out = torch.full((6, 51), 7.0, dtype=DT["bf16"], device="cuda")
+@pytest.mark.parametrize("M,K", [(6, 160), (33, 160), (40, 12320)])
+def test_w4_strided_rows_and_output(M, K):
+    x, codes, scales, zp = dc.w4_inputs(5, "bf16", M, K, 37, 32, True)
+    wide = torch.full((M, K + 40), float("nan"), dtype=DT["bf16"])
+    wide[:, :K] = x
+    out = torch.full((M, 51), 7.0, dtype=DT["bf16"], device="cuda")
     pad = torch.cat([codes, codes[:, :8]], 1)  # strided codes, scales and zero points too
     sc, z = torch.cat([scales, scales], 1), torch.cat([zp, zp], 1)
-    w = lm.linear_w4_prepare(dev(pad)[:, :80], dev(sc)[:, :5], dev(z)[:, :5])
-    lm.linear_w4(dev(wide)[:, :160], w, out=out[:, 3:40])
+    w = lm.linear_w4_prepare(dev(pad)[:, :K // 2], dev(sc)[:, :K // 32], dev(z)[:, :K // 32])
+    lm.linear_w4(dev(wide)[:, :K], w, out=out[:, 3:40])
     ref = oracle.linear_w4(x, codes, scales, zp)
     within(f64(out[:, 3:40]), ref, dc.w4_bound("bf16", x, scales, ref, 32), "y")
     assert torch.all(out[:, :3] == 7.0) and torch.all(out[:, 40:] == 7.0)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-def test_w4_rows_do_not_mix(dtype):
+@pytest.mark.parametrize("K", [256, 16384])
+def test_w4_rows_do_not_mix(dtype, K):
     """A NaN row of x gives a NaN row of y and leaves the others as they were; a NaN scale its own
     column."""
-    x, codes, scales, zp = dc.w4_inputs(9, dtype, 21, 256, 40, 128, True)
+    x, codes, scales, zp = dc.w4_inputs(9, dtype, 21, K, 40, 128, True)
     y0 = _w4(x, codes, scales, zp)
     x[20] = float("nan")
     scales[7, 1] = float("nan")
