@@ -8,13 +8,15 @@
 // kernel. Statistics and outputs are fp32, scores in base 2. Two kinds of tiles run in one launch:
 //
 //   shared (tile_body)  128 query rows (token, head of the group) of one segment against a range of
-//     its prefix, when segments have more than 32 rows on average: 4 waves of 32 rows walk the same
-//     64-key blocks (32 for D > 128), staged once in LDS. The arithmetic of the prefix is bound by
-//     the matrix and exponential pipes and by LDS reads (64 rows x 128 keys of a block cost as many
-//     LDS cycles as matrix cycles).
+//     its prefix, when segments have more than 32 rows on average (37 tokens of 7 heads a key head in 5
+//     segments: 14 us, 18.8 with 16-row tiles): 4 waves of 32 rows walk the same 64-key blocks (32
+//     for D > 128), staged once in LDS. 256 tokens over one 16k prefix run at 663 TFLOP/s; the matrix
+//     pipe is about a quarter busy, the LDS as much, and the rest are waits of a wave's own chain
+//     (scores, softmax, outputs), of which one workgroup per unit hides little.
 //   rows (rows_body)    at most 16 rows: the heads of one token against its own keys, or the rows of a
 //     short prefix tile. Bound by the bytes of the keys: each wave takes 16-key blocks of the range
-//     in turn, with its own statistics, and the waves are joined in LDS at the end.
+//     in turn, with its own statistics, and the waves are joined in LDS at the end. 256 tokens with 1024
+//     keys of their own (8 key heads of 128): 5.2 TB/s, join included.
 //
 // Prefix workgroups come first, about one per compute unit, and leave half of each unit's LDS to
 // the memory-bound ones that follow, which then run beside them.
@@ -495,10 +497,12 @@ __device__ __forceinline__ void static_for(F f) {
 }
 
 // Shared prefix tile: 4 waves of 32 query rows each walk the same key blocks, staged once in LDS for
-// all of them (double buffered, one barrier a block). Per block and wave (D 128, 64 keys) 32 matrix steps
-// of 32 cycles stand against about 170 vector instructions (32 exponentials of 16 cycles among
-// them); the K fragments are read ahead of the scores and the V fragments ahead of the softmax, so that
-// LDS latency passes under arithmetic.
+// all of them (double buffered, one barrier a block). Per block and wave (D 128, 64 keys) there are 32
+// matrix steps of 32 cycles and about 170 vector instructions (32 exponentials among them). A block's
+// offsets are read one block ahead, K fragments before the next loads are issued and V fragments before
+// the softmax, so that LDS latency passes under other work: 508 TFLOP/s without any of that (256 tokens
+// over a 16k prefix), 618 with the fragments, 663 with the offsets. Reading all 8 K steps ahead spills
+// (318); forming the next scores beside the softmax in the same wave was slower too (480).
 template <int DT, int DP>
 __device__ __forceinline__ void tile_body(const PrefixAttnArgs& a, const Work& w, TileLds<DP>& S) {
   constexpr int BK = tile_block<DP>();

@@ -569,7 +569,8 @@ lora_status lora_embedding_a(lora_dtype dtype, int64_t T, int64_t V, int32_t R, 
  *   W[n][k] = scales[n][k / group] * (c[n][k] - z[n][k / group]),
  * c and z in 0..15 (z = 8 without zero points), with fp32 accumulation and one rounding to `dtype`.
  * Few rows is where it is fast (the time is that of reading the weight up to about 16 rows); any M
- * is right. x has to be finite: an infinity gives NaN in its row.
+ * is right. x has to be finite, and below 2^115 in bf16: an infinity, or sums of a group's x times
+ * up to 31 that pass the range of fp32, give NaN or infinities in their row.
  *
  * lora_linear_w4_prepare writes the weight in the layout the product reads, once per layer:
  *   dtype          LORA_BF16 or LORA_F16: the type of x, y and scales.

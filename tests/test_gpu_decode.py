@@ -210,6 +210,8 @@ ATTN = {
     "many rows": (150, [100, 50], 8, 2, 64, 16, [700, 333], [(13 * t) % 70 for t in range(150)], {}),
     "many rows d128": (90, [70, 20], 8, 2, 128, 16, [1500, 640], [(29 * t) % 90 for t in range(90)], {}),
     "many rows d256": (40, [33, 7], 8, 1, 256, 16, [500, 64], [(29 * t) % 90 for t in range(40)], {}),
+    "pages of one place": (9, [9], 8, 2, 128, 1, [300], [(29 * t) % 90 for t in range(9)], {}),
+    "one page each": (20, [20], 8, 2, 64, 1000, [900], [(29 * t) % 90 for t in range(20)], {}),
     "sharp": (12, [12], 8, 2, 128, 16, [900], [(29 * t) % 90 for t in range(12)], dict(std=6.0)),
 }
 
@@ -256,6 +258,39 @@ def test_attention_lengths_beyond_the_lists_are_clamped():
     c.prefix_lens[0] = 2 ** 31 - 1
     c.own_lens[1] = 100
     _check_attn(c, *_attn(c))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30])
+@pytest.mark.parametrize("T", [3, 40])
+def test_attention_other_scales(scale, T):
+    """Equal weights, a negative scale, a tiny one: masked places stay out of all of them."""
+    c = dc.Attn(7, "bf16", T, [T], 8, 2, 128, 16, [100], [(7 * t) % 33 for t in range(T)])
+    c.scale = scale
+    ref, rl, spread = oracle.prefix_attention(*c.args())
+    bo, bl = c.bounds(ref, rl, spread)
+    c.scale = abs(scale)
+    bo2, bl2 = c.bounds(ref, rl, spread)  # the bound takes the magnitude
+    c.scale = scale
+    out, lse = _attn(c)
+    within(f64(out), ref, np.maximum(bo, bo2), "out")
+    within(f64(lse), rl, np.maximum(bl, bl2), "lse")
+
+
+def test_empty_batches():
+    z = lambda *s, d="bf16": torch.zeros(s, dtype=DT.get(d, d), device="cuda")
+    kc = z(2, 4, 2, 64)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+    q = lm.rope_append(z(0, 256), z(0, 128), z(0, 128), dev(dc.table(4, 64)), i32(0),
+                       torch.zeros(0, dtype=torch.int64, device="cuda"), kc, kc.clone())
+    assert q.shape == (0, 256)
+    out, lse = lm.prefix_attention(q, kc, kc, i32(3), None, i32(2, 1), i32(2), i32(0, 1), i32(0), 0.1, return_lse=True)
+    assert out.shape == (0, 256) and lse.shape == (0, 4)
+    mark = torch.full((3, 256), 7.0, dtype=DT["bf16"], device="cuda")  # no segment: nothing is written
+    lm.prefix_attention(z(3, 256), kc, kc, i32(1), None, i32(0, 1), i32(0), i32(3, 1), i32(3), 0.1, out=mark)
+    # a cache without pages: every key is masked, every row empty
+    out = lm.prefix_attention(z(3, 256), kc[:0], kc[:0], dev(torch.tensor([0, 3], dtype=torch.int32)), None, i32(1, 2),
+                              i32(1) + 5, i32(3, 2), i32(3) + 4, 0.1)
+    assert torch.all(mark == 7.0) and torch.all(out == 0)
 
 
 def test_attention_without_prefixes_or_own_keys():
