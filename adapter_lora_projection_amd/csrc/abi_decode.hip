@@ -39,6 +39,8 @@ bool places_overlap(int64_t pages, int64_t ps, int64_t page, int64_t ts, int64_t
   return false;
 }
 
+constexpr int64_t kMaxW4Rows = int64_t(1) << 19;  // 16 rows per workgroup in a 16-bit grid dimension
+
 // Sizes of a 4-bit weight: LORA_OK, or the error of the first one that is wrong.
 lora_status w4_sizes(lora_dtype dtype, int64_t K, int64_t N, int32_t group) {
   if (!is_16bit(dtype)) return LORA_EUNSUPPORTED;
@@ -78,7 +80,7 @@ lora_status lora_linear_w4_prepare(lora_dtype dtype, int64_t K, int64_t N, int32
 }
 
 size_t lora_linear_w4_workspace_size(lora_dtype dtype, int64_t M, int64_t K, int64_t N, int32_t group) {
-  if (w4_sizes(dtype, K, N, group) != LORA_OK || M < 1 || M > (int64_t(1) << 20)) return 0;
+  if (w4_sizes(dtype, K, N, group) != LORA_OK || M < 1 || M > kMaxW4Rows) return 0;
   return lmx::w4_plan(M, K, N, group).workspace;
 }
 
@@ -89,7 +91,7 @@ lora_status lora_linear_w4(lora_dtype dtype, int64_t M, int64_t K, int64_t N, in
   const lora_status st = w4_sizes(dtype, K, N, group);
   if (st != LORA_OK) return st;
   if (M < 0) return LORA_EINVAL;
-  if (M > (int64_t(1) << 20)) return LORA_EUNSUPPORTED;
+  if (M > kMaxW4Rows) return LORA_EUNSUPPORTED;
   if (M == 0) return LORA_OK;
   if (!x || !prepared || !y || ldx < K || ldy < N) return LORA_EINVAL;
   if (!al16(x) || ldx % 8 != 0 || !al16(prepared)) return LORA_EUNSUPPORTED;

@@ -586,7 +586,7 @@ lora_status lora_embedding_a(lora_dtype dtype, int64_t T, int64_t V, int32_t R, 
  *   not overlap x); workspace: device scratch of lora_linear_w4_workspace_size(...) bytes (partial
  *   sums of ranges of K; 0 for one or two rows, and wherever one launch is faster), 16-byte aligned, not
  *   read before written. Calls that overlap in time must not share it.
- * Errors: LORA_EUNSUPPORTED (dtype, group, K or N above 2^24, M above 2^20, unaligned x or
+ * Errors: LORA_EUNSUPPORTED (dtype, group, K or N above 2^24, M above 2^19, unaligned x or
  * prepared), LORA_EINVAL (sizes, K % group, pitches, null pointers), LORA_EWORKSPACE (prepared or
  * workspace too small or unaligned), LORA_EHIP. lora_linear_w4_prepared_size returns 0 for sizes that are refused.
  */

@@ -37,7 +37,7 @@ def _w4(**kw):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(dtype=0), EUNSUP), (dict(M=-1), EINVAL), (dict(M=(1 << 20) + 1), EUNSUP), (dict(K=250), EINVAL),
+    (dict(dtype=0), EUNSUP), (dict(M=-1), EINVAL), (dict(M=(1 << 19) + 1), EUNSUP), (dict(K=250), EINVAL),
     (dict(group=16), EUNSUP), (dict(x=None), EINVAL), (dict(w=None), EINVAL), (dict(y=None), EINVAL),
     (dict(ldx=255), EINVAL), (dict(ldx=260), EUNSUP), (dict(ldy=31), EINVAL), (dict(x=0x1002), EUNSUP),
     (dict(w=0x2008), EUNSUP), (dict(M=0, x=None, y=None), OK),
