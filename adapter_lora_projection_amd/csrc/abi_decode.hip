@@ -226,7 +226,7 @@ lora_status lora_prefix_attention(lora_dtype dtype, int64_t T, int32_t G, int32_
   a.by_prefix_splits = lmx::FastDiv::of(p.prefix_splits);
   a.by_own_tiles = lmx::FastDiv::of(p.own_tiles); a.by_own_splits = lmx::FastDiv::of(p.own_splits);
   a.out8 = (reinterpret_cast<uintptr_t>(out) & 7u) == 0 && ldo % 4 == 0;
-  a.shared = p.shared; a.prefix_unit = p.prefix_unit; a.own_unit = p.own_unit;
+  a.direct = p.direct; a.shared = p.shared; a.prefix_unit = p.prefix_unit; a.own_unit = p.own_unit;
   // the kernels multiply masked scores (-inf) by it: above 0, with the sign in the queries (a scale of
   // 0 gives equal weights, and so does 2^-100)
   a.negate = scale < 0.f;

@@ -16,7 +16,7 @@
 //   rows (rows_body)    at most 16 rows: the heads of one token against its own keys, or the rows of a
 //     short prefix tile. Bound by the bytes of the keys: each wave takes 16-key blocks of the range
 //     in turn, with its own statistics, and the waves are joined in LDS at the end. 256 tokens with 1024
-//     keys of their own (8 key heads of 128): 5.2 TB/s, join included.
+//     keys of their own (8 key heads of 128): 5.7 TB/s.
 //
 // Prefix workgroups come first, about one per compute unit, and leave half of each unit's LDS to
 // the memory-bound ones that follow, which then run beside them.
@@ -254,6 +254,27 @@ __device__ __forceinline__ float add_wave(float v) {
   return add_groups(v);
 }
 
+// Four output elements of one row, to be followed by their row's other pieces.
+template <int DT>
+__device__ __forceinline__ void store_out(const PrefixAttnArgs& a, int tok, int head, int d, float4 v) {
+  uint16_t* op = static_cast<uint16_t*>(a.out) + int64_t(tok) * a.ldo + int64_t(head) * a.D + d;
+  const uint32_t lo = cvt2<DT>(v.x, v.y), hi = cvt2<DT>(v.z, v.w);
+  if (a.out8) {
+    *reinterpret_cast<uint2*>(op) = make_uint2(lo, hi);
+  } else {
+    op[0] = uint16_t(lo);
+    op[1] = uint16_t(lo >> 16);
+    op[2] = uint16_t(hi);
+    op[3] = uint16_t(hi >> 16);
+  }
+}
+__device__ __forceinline__ void store_lse(const PrefixAttnArgs& a, int tok, int head, float m, float l) {
+  if (a.lse != nullptr)
+    a.lse[int64_t(tok) * a.Hq + head] = l == 0.f ? kNegInf : (m + __log2f(l)) * 0.6931471805599453f;
+}
+// Of a row's sum: no visible key gives zeros (a NaN sum stays NaN).
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
 constexpr int kWaves = 4;
 constexpr int kTabKeys = 256;  // keys covered by one fill of a wave's offset table
 
@@ -270,9 +291,10 @@ template <int DP>
 struct RowsLds {
   RowsWave<DP> wave[kWaves];
   float2 ml[kWaves][16];
+  float inv[16];
 };
 
-template <int DT, int DP>
+template <int DT, int DP, bool DIRECT>
 __device__ __forceinline__ void rows_body(const PrefixAttnArgs& a, const Work& w, RowsLds<DP>& S) {
   constexpr int NB = RowsWave<DP>::kBufs;
   constexpr int CPR = DP / 8;         // 16-byte chunks per key row
@@ -433,6 +455,7 @@ __device__ __forceinline__ void rows_body(const PrefixAttnArgs& a, const Work& w
 #pragma unroll
   for (int x = 0; x < kWaves; ++x) ll += S.ml[x][col].y * __builtin_amdgcn_exp2f(S.ml[x][col].x - base);
   const float f = __builtin_amdgcn_exp2f(m - base);
+  if (DIRECT && wave == 0 && grp == 0) S.inv[col] = inverse(ll);
   // [16 rows][DP + 4] fp32 per wave, over the wave's own (now idle) buffers and table
   constexpr int OP = DP + 4;
   static_assert(sizeof(RowsWave<DP>) >= sizeof(float) * 16 * OP, "join buffer");
@@ -452,12 +475,20 @@ __device__ __forceinline__ void rows_body(const PrefixAttnArgs& a, const Work& w
       v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
     }
     const int rr = w.row0 + r;
-    const int rp = a.by_grp.div(rr);
-    const int64_t prow = int64_t(rp) * a.Hq + w.kvh * a.grp + rr - rp * a.grp;
+    const int rp = a.by_grp.div(rr), rh = w.kvh * a.grp + rr - rp * a.grp;
+    if constexpr (DIRECT) {  // the only range of its row
+      const float inv = S.inv[r];
+      store_out<DT>(a, a.permutation != nullptr ? a.permutation[rp] : rp, rh, d,
+                    make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+      continue;
+    }
+    const int64_t prow = int64_t(rp) * a.Hq + rh;
     *reinterpret_cast<float4*>(a.part_o + (int64_t(w.slot) * rows_all + prow) * a.D + d) = v;
   }
-  if (wave == 0 && grp == 0 && row_ok)
-    a.part_ml[int64_t(w.slot) * rows_all + int64_t(pos) * a.Hq + head] = make_float2(mm, ll);
+  if (wave == 0 && grp == 0 && row_ok) {
+    if constexpr (DIRECT) store_lse(a, tok, head, mm, ll);
+    else a.part_ml[int64_t(w.slot) * rows_all + int64_t(pos) * a.Hq + head] = make_float2(mm, ll);
+  }
 }
 
 
@@ -743,23 +774,35 @@ __device__ __forceinline__ void tile_body(const PrefixAttnArgs& a, const Work& w
   if (half == 0) a.part_ml[int64_t(w.slot) * rows_all + prow] = make_float2(m, l);
 }
 
-// One workgroup per (row tile, key head, key range); LDS is whichever layout its tile needs.
-template <int DT, int DP>
+// One workgroup per (row tile, key head, key range); LDS is whichever layout its tile needs. DIRECT: no
+// prefix and one range per row, which goes to the output at once (256 tokens with 1024 keys each: 191 us,
+// 206 with a plane and the join).
+template <int DT, int DP, bool DIRECT>
 __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void prefix_attn_kernel(PrefixAttnArgs a) {
-  constexpr size_t kLds = sizeof(TileLds<DP>) > sizeof(RowsLds<DP>) ? sizeof(TileLds<DP>) : sizeof(RowsLds<DP>);
+  constexpr size_t kLds = DIRECT || sizeof(RowsLds<DP>) > sizeof(TileLds<DP>) ? sizeof(RowsLds<DP>) : sizeof(TileLds<DP>);
   __shared__ __align__(1024) unsigned char s_mem[kLds];
   const Work w = find_work(a, int(blockIdx.x));
-  if (w.k1 <= w.k0) {  // no keys in this range: its rows say so to the join
+  if (w.k1 <= w.k0) {  // no keys in this range: its rows say so to the join, or are zeros
     const int64_t rows_all = int64_t(a.T) * a.Hq;
     for (int r = int(threadIdx.x); r < w.nrows; r += 64 * kWaves) {
-      const int row = w.row0 + r, pos = a.by_grp.div(row);
-      a.part_ml[int64_t(w.slot) * rows_all + int64_t(pos) * a.Hq + w.kvh * a.grp + row - pos * a.grp] =
-          make_float2(kNegInf, 0.f);
+      const int row = w.row0 + r, pos = a.by_grp.div(row), head = w.kvh * a.grp + row - pos * a.grp;
+      if constexpr (DIRECT) {
+        const int tok = a.permutation != nullptr ? a.permutation[pos] : pos;
+        for (int d = 0; d < a.D; d += 4) store_out<DT>(a, tok, head, d, make_float4(0.f, 0.f, 0.f, 0.f));
+        store_lse(a, tok, head, kNegInf, 0.f);
+      } else {
+        a.part_ml[int64_t(w.slot) * rows_all + int64_t(pos) * a.Hq + head] = make_float2(kNegInf, 0.f);
+      }
     }
     return;
   }
-  if (w.shared) tile_body<DT, DP>(a, w, *reinterpret_cast<TileLds<DP>*>(s_mem));
-  else rows_body<DT, DP>(a, w, *reinterpret_cast<RowsLds<DP>*>(s_mem));
+  if constexpr (!DIRECT) {
+    if (w.shared) {
+      tile_body<DT, DP>(a, w, *reinterpret_cast<TileLds<DP>*>(s_mem));
+      return;
+    }
+  }
+  rows_body<DT, DP, DIRECT>(a, w, *reinterpret_cast<RowsLds<DP>*>(s_mem));
 }
 
 // Joins the key ranges of every (sorted position, query head): one wave per row. 64 ranges at a
@@ -824,21 +867,9 @@ __global__ __launch_bounds__(256) void prefix_attn_join_kernel(PrefixAttnArgs a)
     tot.x += __shfl(acc.x, src, 64); tot.y += __shfl(acc.y, src, 64);
     tot.z += __shfl(acc.z, src, 64); tot.w += __shfl(acc.w, src, 64);
   }
-  const float inv = ll == 0.f ? 0.f : 1.f / ll;  // no visible key: zeros (a NaN sum stays NaN)
-  uint16_t* op = static_cast<uint16_t*>(a.out) + int64_t(tok) * a.ldo + int64_t(h) * a.D;
-  if (lane < pieces) {
-    const uint32_t lo = cvt2<DT>(tot.x * inv, tot.y * inv), hi = cvt2<DT>(tot.z * inv, tot.w * inv);
-    if (a.out8) {
-      *reinterpret_cast<uint2*>(op + lane * 4) = make_uint2(lo, hi);
-    } else {
-      op[lane * 4] = uint16_t(lo);
-      op[lane * 4 + 1] = uint16_t(lo >> 16);
-      op[lane * 4 + 2] = uint16_t(hi);
-      op[lane * 4 + 3] = uint16_t(hi >> 16);
-    }
-  }
-  if (a.lse != nullptr && lane == 0)
-    a.lse[int64_t(tok) * a.Hq + h] = ll == 0.f ? kNegInf : (mm + __log2f(ll)) * 0.6931471805599453f;
+  const float inv = inverse(ll);
+  if (lane < pieces) store_out<DT>(a, tok, h, lane * 4, make_float4(tot.x * inv, tot.y * inv, tot.z * inv, tot.w * inv));
+  if (lane == 0) store_lse(a, tok, h, mm, ll);
 }
 
 int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -847,8 +878,12 @@ template <int DT, int DP>
 hipError_t launch_dp(const PrefixAttnArgs& a, hipStream_t st) {
   const int64_t grid = int64_t(a.Hkv) * (int64_t(a.prefix_tiles) * a.prefix_splits +
                                          int64_t(a.T) * a.own_tiles * a.own_splits);
+  if (a.direct) {
+    hipLaunchKernelGGL((prefix_attn_kernel<DT, DP, true>), dim3(unsigned(grid)), dim3(64 * kWaves), 0, st, a);
+    return hipGetLastError();
+  }
   if (grid > 0)
-    hipLaunchKernelGGL((prefix_attn_kernel<DT, DP>), dim3(unsigned(grid)), dim3(64 * kWaves), 0, st, a);
+    hipLaunchKernelGGL((prefix_attn_kernel<DT, DP, false>), dim3(unsigned(grid)), dim3(64 * kWaves), 0, st, a);
   hipLaunchKernelGGL((prefix_attn_join_kernel<DT>), dim3(unsigned(cdiv64(int64_t(a.T) * a.Hq, 4))),
                      dim3(256), 0, st, a);
   return hipGetLastError();
@@ -882,7 +917,9 @@ PrefixAttnPlan prefix_attention_plan(int64_t T, int G, int Hq, int Hkv, int D, i
   p.prefix_splits = int(splits(pmax, ptiles * Hkv, p.shared ? 256 : 512, p.shared ? 256 : 64));
   const int64_t left = std::max<int64_t>(256, 512 - ptiles * Hkv * p.prefix_splits);
   p.own_splits = int(splits(omax, T * p.own_tiles * Hkv, left, 64));
-  const int64_t rows = T * Hq, slots = p.prefix_splits + p.own_splits;
+  // one range a row and no prefix: the rows are written as they are
+  p.direct = p.prefix_splits == 0 && p.own_splits == 1;
+  const int64_t rows = p.direct ? 0 : T * Hq, slots = p.prefix_splits + p.own_splits;
   p.part_ml = size_t(slots * rows * D * 4 + 255) & ~size_t(255);
   p.total = p.part_ml + size_t(slots * rows * 8);
   return p;

@@ -50,6 +50,7 @@ struct PrefixAttnArgs {
   int own_tiles, own_splits;        // row tiles per token and key ranges of the own part
   int prefix_unit, own_unit;        // keys that a range is a multiple of
   int shared;                       // prefix tiles of 128 rows, else 16
+  int direct;                       // one key range a row: no partials, no join
   int out8;                         // output rows are 8-byte aligned
   int negate;                       // scale < 0: the queries' signs are flipped
   float scale_log2;                 // |scale| * log2(e), above 0
@@ -60,6 +61,7 @@ struct PrefixAttnArgs {
 struct PrefixAttnPlan {
   int dp;  // head size rounded up to 64, 128 or 256
   bool shared;  // prefix tiles of 128 rows sharing their key blocks (else 16 rows)
+  bool direct;  // one key range per row, written to the output at once
   int prefix_tiles, prefix_splits, prefix_unit, own_tiles, own_splits, own_unit;
   size_t part_ml, total;  // workspace: byte offset of part_ml, total bytes
 };

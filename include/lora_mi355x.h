@@ -683,7 +683,8 @@ lora_status lora_rope_append(lora_dtype dtype, int64_t T, int32_t Hq, int32_t Hk
  *   out            device [T][ldo >= Hq*D], any alignment.
  *   lse            device float [T][Hq] (natural logarithm) or NULL.
  *   workspace      device scratch of lora_prefix_attention_workspace_size(...) bytes (partial outputs
- *                  of the key ranges), 16-byte aligned; not read before written. Calls that overlap in
+ *                  of the key ranges; 0 without prefixes where one range per row fills the GPU),
+ *                  16-byte aligned; not read before written. Calls that overlap in
  *                  time must not share it.
  * The number of key ranges follows from the widths, so pass lists no wider than the longest length
  * needs. Results do not depend on timing.

@@ -337,6 +337,30 @@ def test_refusals_of_the_library_on_the_gpu():
     assert torch.all(out == 7.0)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,Hq,Hkv,D,page,first,layout", [
+    (70, 16, 8, 128, 16, 0, "phd"), (70, 8, 8, 64, 3, 2, "hpd"), (40, 40, 20, 80, 24, 1, "phd"),
+    (80, 80, 8, 256, 16, 0, "phd"), (600, 20, 1, 64, 32, 0, "phd"),
+])
+def test_attention_one_range_per_row(dtype, T, Hq, Hkv, D, page, first, layout):
+    """Enough rows for one key range each and no prefix: written without a join. Rows without keys,
+    rows without a segment, output rows off the 8-byte grid, pages outside the cache."""
+    own = [(17 * t) % 70 for t in range(T)]
+    own[T // 2] = 0
+    c = dc.Attn(T + D, dtype, T, [T // 2, T - first - T // 2 - 1], Hq, Hkv, D, page, [0, 0], own, indptr0=first, layout=layout)
+    c.own_pages[5, 0] = -1
+    a = list(c.args(dev))
+    a[5] = a[6] = None
+    mark = torch.full((T, Hq * D + 3), 7.0, dtype=DT[dtype], device="cuda")
+    assert lm.prefix_attention_workspace(a[0], a[1], a[3], None, a[7]).numel() == 0
+    out, lse = lm.prefix_attention(*a, return_lse=True, out=mark[:, 1:1 + Hq * D])
+    cov = _check_attn(c, out, lse)
+    assert cov.sum() == T - first - 1 and torch.all(out[torch.from_numpy(~cov).cuda()] == 7.0)
+    assert torch.all(mark[:, 0] == 7.0) and torch.all(mark[:, 1 + Hq * D:] == 7.0)
+    aligned = lm.prefix_attention(*a)
+    assert torch.equal(aligned[torch.from_numpy(cov).cuda()], out[torch.from_numpy(cov).cuda()])
+
+
 def test_attention_same_sequence_several_tokens():
     """Tokens of one sequence as rows that repeat its pages with lengths rising by one."""
     c = dc.Attn(9, "bf16", 6, [6], 8, 2, 128, 16, [100], [37] * 6)
