@@ -30,11 +30,11 @@ bool places_overlap(int64_t pages, int64_t ps, int64_t page, int64_t ts, int64_t
   for (int i = 0; i < 2; ++i)
     for (int j = i + 1; j < 3; ++j)
       if (s[j] < s[i]) { std::swap(s[i], s[j]); std::swap(n[i], n[j]); }
-  int64_t span = D;
+  __int128 span = D;
   for (int i = 0; i < 3; ++i) {
     if (n[i] <= 1) continue;
     if (s[i] < span) return true;
-    span = s[i] * (n[i] - 1) + span;
+    span += __int128(s[i]) * (n[i] - 1);
   }
   return false;
 }
@@ -121,7 +121,9 @@ lora_status lora_rope_append(lora_dtype dtype, int64_t T, int32_t Hq, int32_t Hk
     return LORA_EINVAL;
   if (!std::isfinite(eps) || eps < 0.f) return LORA_EINVAL;
   if (D > 1024 || Hq > 65536 || Hkv > 65536 || table_rows >= INT_MAX) return LORA_EUNSUPPORTED;
-  if (T * (int64_t(Hq) + 2 * Hkv) > (int64_t(1) << 30) || num_pages > (int64_t(1) << 40)) return LORA_EUNSUPPORTED;
+  // up to 64 lanes a head in a launch of less than 2^32 threads; slots are 64-bit
+  if (T >= (int64_t(1) << 26) || T * (int64_t(Hq) + 2 * Hkv) >= (int64_t(1) << 26)) return LORA_EUNSUPPORTED;
+  if (num_pages > INT64_MAX / page_size) return LORA_EUNSUPPORTED;
   if (T == 0) return LORA_OK;
   if ((Hq > 0 && (!q || !q_out)) || !k || !v || !table || !positions || !slots) return LORA_EINVAL;
   if (num_pages > 0 && (!k_cache || !v_cache)) return LORA_EINVAL;

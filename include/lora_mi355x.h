@@ -636,7 +636,7 @@ size_t lora_linear_w4_workspace_size(lora_dtype dtype, int64_t M, int64_t K, int
  *                  [page][head][place][d] storage fit.
  * Any alignment; rows, weights and cache rows that are all 16-byte aligned, with D % 8 == 0 and
  * rot % 16 == 0, take the vector form. One launch, no workspace.
- * Errors: LORA_EUNSUPPORTED (dtype, D > 1024, T * (Hq + 2 Hkv) > 2^30), LORA_EINVAL (sizes, strides,
+ * Errors: LORA_EUNSUPPORTED (dtype, D > 1024, T * (Hq + 2 Hkv) >= 2^26), LORA_EINVAL (sizes, strides,
  * eps, null pointers), LORA_EHIP.
  */
 lora_status lora_rope_append(lora_dtype dtype, int64_t T, int32_t Hq, int32_t Hkv, int32_t D,

@@ -88,6 +88,16 @@ def test_rope_refusals(kw, code):
     assert _rope(**kw) == code
 
 
+@pytest.mark.parametrize("kw,code", [
+    # more heads than a launch has threads for, and products of sizes beyond 64 bits
+    (dict(T=1 << 23), EUNSUP), (dict(T=1 << 62, Hq=0, Hkv=2), EUNSUP), (dict(T=1 << 61), EUNSUP),
+    (dict(pages=1 << 40, page=1 << 30, ps=128 << 30), EUNSUP),
+    (dict(pages=4, page=2, hs=1 << 62, ts=64, ps=1 << 62), EINVAL),  # the second page on the second head
+])
+def test_rope_refuses_sizes_beyond_a_launch(kw, code):
+    assert _rope(**kw) == code
+
+
 def _attn(**kw):
     a = dict(dtype=1, T=4, G=2, Hq=4, Hkv=2, D=64, pages=8, page=16, q=0x1000, ldq=256, kc=0x2000, vc=0x3000,
              ps=16 * 128, ts=128, hs=64, indptr=0x4000, perm=None, pp=0x5000, wp=4, pl=0x6000, op=0x7000, wo=4,
