@@ -163,7 +163,7 @@ lora_status attn_sizes(lora_dtype dtype, int64_t T, int32_t G, int32_t Hq, int32
   // 32-bit key indexes and row counts in the kernels
   constexpr int64_t kMaxKeys = int64_t(1) << 30;
   if (prefix_width > kMaxKeys / page_size || own_width > kMaxKeys / page_size) return LORA_EUNSUPPORTED;
-  if (T > (int64_t(1) << 24) || G > (1 << 24) || T * Hq > (int64_t(1) << 26)) return LORA_EUNSUPPORTED;
+  if (T > (int64_t(1) << 24) || G > (1 << 24) || T * Hq >= (int64_t(1) << 26)) return LORA_EUNSUPPORTED;
   return LORA_OK;
 }
 
@@ -209,7 +209,7 @@ lora_status lora_prefix_attention(lora_dtype dtype, int64_t T, int32_t G, int32_
   if (p.total > 0 && (workspace == nullptr || workspace_bytes < p.total || !al16(workspace)))
     return LORA_EWORKSPACE;
   const int64_t wgs = int64_t(Hkv) * (int64_t(p.prefix_tiles) * p.prefix_splits + T * p.own_tiles * p.own_splits);
-  if (wgs >= INT_MAX) return LORA_EUNSUPPORTED;
+  if (wgs >= (int64_t(1) << 24)) return LORA_EUNSUPPORTED;  // of 256 threads, of which a launch takes under 2^32
   lmx::PrefixAttnArgs a{};
   a.q = q; a.k_cache = k_cache; a.v_cache = v_cache; a.seg_indptr = seg_indptr;
   a.permutation = permutation; a.prefix_pages = prefix_pages; a.prefix_lens = prefix_lens;

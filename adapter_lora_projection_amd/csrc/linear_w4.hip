@@ -351,6 +351,7 @@ W4Plan w4_plan(int64_t M, int64_t K, int64_t N, int group) {
   const int64_t slabs = (N + 128 * nt - 1) / (128 * nt), mb = (M + 16 * mt - 1) / (16 * mt);
   for (int64_t want = 1; want <= std::min<int64_t>(kt, 64); want *= 2) {
     const int64_t per = (kt + want - 1) / want, r = (kt + per - 1) / per;  // no empty ranges at the end
+    if (r > 1 && M * ntiles >= int64_t(1) << 29) break;  // four columns a thread, under 2^31 threads in w4_sum_kernel
     double c = rounds(slabs * mb * r) * double(per) * double(8 * nt * 1088 + 4096 * mt);
     if (r > 1) c += rounds(slabs * mb * r) * 8192.0 * nt * mt + double(r * M * ntiles * 16 * 4) / 256;
     c = c / 25 + (r > 1 ? 6500 : 0);

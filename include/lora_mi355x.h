@@ -689,7 +689,7 @@ lora_status lora_rope_append(lora_dtype dtype, int64_t T, int32_t Hq, int32_t Hk
  * The number of key ranges follows from the widths, so pass lists no wider than the longest length
  * needs. Results do not depend on timing.
  * Errors: LORA_EUNSUPPORTED (dtype, D, unaligned q or cache, width * page_size > 2^30,
- * T * Hq > 2^26), LORA_EINVAL (sizes, strides, a scale that is not finite, null pointers),
+ * T * Hq >= 2^26, 2^24 or more row tiles x key heads), LORA_EINVAL (sizes, strides, a scale that is not finite, null pointers),
  * LORA_EWORKSPACE, LORA_EHIP.
  */
 lora_status lora_prefix_attention(lora_dtype dtype, int64_t T, int32_t G, int32_t Hq, int32_t Hkv,

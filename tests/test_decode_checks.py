@@ -124,6 +124,14 @@ def test_attention_refusals(kw, code):
     assert _attn(**kw) == code
 
 
+@pytest.mark.parametrize("kw", [
+    dict(T=1 << 24, Hq=4, Hkv=1),             # one thread too many in the join
+    dict(T=1 << 23, Hq=4, Hkv=4, ldq=256),    # a workgroup per token and key head, of 256 threads
+])
+def test_attention_refuses_batches_beyond_a_launch(kw):
+    assert _attn(wp=0, nbytes=1 << 60, **kw) == EUNSUP
+
+
 def test_attention_workspace_query():
     size = _lib.lora_prefix_attention_workspace_size
     assert size(1, 4, 2, 4, 2, 64, 16, 4, 4) > 0
