@@ -899,7 +899,7 @@ PrefixAttnPlan prefix_attention_plan(int64_t T, int G, int Hq, int Hkv, int D, i
   const int64_t pmax = prefix_width * page_size, omax = own_width * page_size;
   p.shared = T * grp > 32 * int64_t(G);
   const int tile = p.shared ? kTileRows : kRows;
-  p.prefix_tiles = int(cdiv64(T * grp, tile) + G);
+  p.prefix_tiles = int(cdiv64(T * grp, tile) + std::min<int64_t>(G, T));  // a segment of no rows has no tile
   p.own_tiles = int(cdiv64(grp, kRows));
   p.own_unit = 16 * kWaves;
   p.prefix_unit = p.shared ? (p.dp > 128 ? tile_block<256>() : tile_block<128>()) : p.own_unit;

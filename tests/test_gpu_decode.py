@@ -361,6 +361,17 @@ def test_attention_one_range_per_row(dtype, T, Hq, Hkv, D, page, first, layout):
     assert torch.equal(aligned[torch.from_numpy(cov).cuda()], out[torch.from_numpy(cov).cuda()])
 
 
+@pytest.mark.parametrize("T,Hq,Hkv", [(3, 4, 2), (9, 16, 1), (70, 8, 1)])
+def test_attention_many_empty_segments(T, Hq, Hkv):
+    """More segments than rows, and rows in the first, a middle and the last of them."""
+    lens = [0] * 300
+    lens[0], lens[150], lens[299] = 1, T - 2, 1
+    c = dc.Attn(T, "bf16", T, lens, Hq, Hkv, 64, 16, [(7 * g) % 90 for g in range(300)], [5] * T)
+    print("segments", T, Hq, Hkv, flush=True)
+    out, lse = lm.prefix_attention(*c.args(dev), return_lse=True)
+    assert _check_attn(c, out, lse).all()
+
+
 def test_attention_same_sequence_several_tokens():
     """Tokens of one sequence as rows that repeat its pages with lengths rising by one."""
     c = dc.Attn(9, "bf16", 6, [6], 8, 2, 128, 16, [100], [37] * 6)
