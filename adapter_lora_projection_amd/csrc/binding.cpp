@@ -96,6 +96,22 @@ at::Tensor output(const at::Tensor* given, int64_t rows, int64_t cols, const at:
   return *given;
 }
 
+// Refuses an output of which an element may be one of the matrix `in`. Column blocks of one buffer (equal
+// pitches) are told apart; other interleavings are not.
+void no_overlap(const at::Tensor& out, const at::Tensor& in, const char* oname, const char* iname) {
+  if (out.numel() == 0 || in.numel() == 0) return;
+  const int64_t lo = pitch(out, oname), li = pitch(in, iname);
+  const int64_t eo = (out.size(0) - 1) * lo + out.size(1), ei = (in.size(0) - 1) * li + in.size(1);
+  const int64_t size = int64_t(out.element_size());
+  const int64_t d = reinterpret_cast<intptr_t>(out.data_ptr()) - reinterpret_cast<intptr_t>(in.data_ptr());
+  if (d >= ei * size || -d >= eo * size) return;
+  if (out.size(0) > 1 && in.size(0) > 1 && lo == li) {
+    const int64_t c = ((d % (lo * size)) + lo * size) % (lo * size);  // where out's columns start in in's rows
+    if (c >= in.size(1) * size && c + out.size(1) * size <= lo * size) return;
+  }
+  refuse(std::string(oname) + " must not overlap " + iname);
+}
+
 // The pair of caches [pages][page size][heads][D], of one shape and strides.
 struct Cache {
   int64_t pages, page, heads, D, ps, ts, hs;
@@ -164,6 +180,7 @@ PyObject* linear_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     vector_of(data, at::kByte, -1, "data");
     if (size_t(data.numel()) < lora_linear_w4_prepared_size(dt, K, N, group, zp)) refuse("data is not a weight of these sizes");
     if (given != nullptr) output(given, x.size(0), N, x, "out");
+    if (given != nullptr) no_overlap(*given, x, "out", "x");
     const int dev = device_of({&x, &data, given});
     const at::Tensor out = output(given, x.size(0), N, x, "out");
     const int64_t ldy = pitch(out, "out");
@@ -207,6 +224,7 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     vector_of(positions, at::kInt, T, "positions");
     vector_of(slots, at::kLong, T, "slots");
     if (given != nullptr) output(given, T, nq, q, "q_out");
+    if (given != nullptr && (given->data_ptr() != q.data_ptr() || pitch(*given, "q_out") != ldq)) no_overlap(*given, q, "q_out", "q");
     const int dev = device_of({&q, &k, &v, &table, &positions, &slots, &kc, &vc, qn, kn, given});
     const at::Tensor out = output(given, T, nq, q, "q_out");
     const int64_t ldqo = pitch(out, "q_out");
@@ -258,6 +276,7 @@ PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t wo = page_list(op, ol, T, "own_pages", "own_lens");
     if (given != nullptr) output(given, T, nq, q, "out");
     if (ws != nullptr) vector_of(*ws, at::kByte, -1, "workspace");
+    if (given != nullptr) no_overlap(*given, q, "out", "q");
     const int dev = device_of({&q, &kc, &vc, &indptr, perm, pp, pl, op, ol, given, ws});
     const int32_t Hq = narrow(nq / c.D, "q"), Hkv = narrow(c.heads, "k_cache"), D = narrow(c.D, "k_cache");
     const int32_t page = narrow(c.page, "k_cache"), g = narrow(G, "seg_indptr");

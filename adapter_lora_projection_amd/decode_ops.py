@@ -79,7 +79,7 @@ def linear_w4_prepare(codes, scales, zero_points=None) -> W4Weight:
 def linear_w4(x, w: W4Weight, out: torch.Tensor | None = None) -> torch.Tensor:
     """y = x W^T with a 4-bit weight (``lora_linear_w4``), for few rows of x: the base product of
     a quantised layer, which ``shrink_expand`` then updates. x: [M][K] of the weight's dtype;
-    returns [M][N]."""
+    returns [M][N] (out, which must not overlap x)."""
     return _result("lora_linear_w4", (_native or _load()).linear_w4(
         x, w.data, ops._DT[w.dtype], w.K, w.N, w.group, w.zero_points, out))
 
@@ -92,7 +92,8 @@ def rope_append(q, k, v, table, positions, slots, k_cache, v_cache, q_norm=None,
     table: float32 [rows][rot], rot / 2 cosines then rot / 2 sines a row; positions: int32 [T], rows of
     the table; slots: int64 [T], place page * page_size + offset, -1: not appended; caches
     [pages][page_size][Hkv][D], written in place; q_norm, k_norm: [D]. Pairs are (p, p + rot / 2), or
-    (2p, 2p + 1) when interleaved. Returns the rotated q [T][Hq*D] (q_out, which may be q)."""
+    (2p, 2p + 1) when interleaved. Returns the rotated q [T][Hq*D] (q_out, which may be q and
+    must not overlap it otherwise)."""
     return _result("lora_rope_append", (_native or _load()).rope_append(
         q, k, v, table, positions, slots, k_cache, v_cache, q_norm, k_norm, eps, interleaved, q_out))
 
@@ -118,7 +119,7 @@ def prefix_attention(q, k_cache, v_cache, seg_indptr, permutation, prefix_pages,
     prefix_lens int32 [G] (None: no prefix); own_pages int32 [T][width] and own_lens int32 [T]: the
     keys of each token after the prefix. Returns out [T][Hq*D], with return_lse also the natural
     logarithm of the softmax sums, float32 [T][Hq]; rows no segment covers are not written.
-    workspace: from ``prefix_attention_workspace`` (a fresh one otherwise)."""
+    out must not overlap q. workspace: from ``prefix_attention_workspace`` (a fresh one otherwise)."""
     return _result("lora_prefix_attention", (_native or _load()).prefix_attention(
         q, k_cache, v_cache, seg_indptr, permutation, prefix_pages, prefix_lens, own_pages, own_lens,
         scale, out, return_lse, workspace))

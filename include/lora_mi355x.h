@@ -680,7 +680,7 @@ lora_status lora_rope_append(lora_dtype dtype, int64_t T, int32_t Hq, int32_t Hk
  *                  own_width 0.
  *                  Lengths are clamped to [0, width * page_size]. The places of a page id outside
  *                  [0, num_pages) are masked; entries beyond a list's length are not read.
- *   out            device [T][ldo >= Hq*D], any alignment.
+ *   out            device [T][ldo >= Hq*D], any alignment; must not overlap q.
  *   lse            device float [T][Hq] (natural logarithm) or NULL.
  *   workspace      device scratch of lora_prefix_attention_workspace_size(...) bytes (partial outputs
  *                  of the key ranges; 0 without prefixes where one range per row fills the GPU),

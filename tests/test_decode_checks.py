@@ -243,6 +243,25 @@ def test_attention_wrapper(kw):
     _refused(lambda: d.prefix_attention(**_attn_tensors(**kw)))
 
 
+def test_outputs_must_not_overlap_inputs():
+    buf = torch.zeros(4 * 256, dtype=bf)
+    w = d.W4Weight(torch.zeros(4 * 1024 + 256, dtype=torch.uint8), bf, 64, 64, 64, False)
+    x = buf[:256].view(4, 64)
+    wide = buf.view(4, 256)
+    for out in (x, buf[64:320].view(4, 64), wide[:, 32:96]):
+        _refused(lambda: d.linear_w4(x, w, out))
+    _refused(lambda: d.linear_w4(wide[:, :64], w, wide[:, 40:104]))
+    for xx, out in ((wide[:, :64], wide[:, 64:128]), (wide[:, 192:], wide[:, :64]), (x, buf[256:512].view(4, 64))):
+        with pytest.raises(ValueError, match="GPU"):  # nothing left but the device
+            d.linear_w4(xx, w, out)
+    q = torch.zeros(4, 128, dtype=bf)
+    _refused(lambda: d.prefix_attention(**_attn_tensors(q=q[:3], out=q[:3])))
+    _refused(lambda: d.prefix_attention(**_attn_tensors(q=q[:3], out=q[1:])))
+    _refused(lambda: d.rope_append(**_rope_tensors(q=q[:3], q_out=q[1:])))
+    with pytest.raises(ValueError, match="GPU"):
+        d.rope_append(**_rope_tensors(q=q[:3], q_out=q[:3]))
+
+
 @pytest.mark.parametrize("kw", [dict(q="x"), dict(k_cache=None), dict(scale="x"), dict(own_pages=3)])
 def test_attention_wrapper_types(kw):
     _refused(lambda: d.prefix_attention(**_attn_tensors(**kw)), TypeError)
